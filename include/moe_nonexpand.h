@@ -69,7 +69,7 @@ extern "C" {
 /* Host return codes. */
 #define MOE_OK 0
 #define MOE_ERR_ARG 1         /* null required pointer, bad N/K/E, bad enum, misaligned pointer */
-#define MOE_ERR_SHAPE 2       /* H or I not a multiple of 64, or sizes overflow 32-bit indexing */
+#define MOE_ERR_SHAPE 2       /* a size no multiple of what the call needs (bf16 forward: H or I of 64), or out of range */
 #define MOE_ERR_WS 3          /* workspace too small (or null) */
 #define MOE_ERR_CUDA 4        /* a CUDA runtime call or launch failed */
 #define MOE_ERR_DEVICE 5      /* current device is not sm_100 (B200-class) */
@@ -488,6 +488,122 @@ typedef struct moe_ep_sources_t {
  */
 MOE_API int moe_ep_combine(const moe_ep_sources_t *src, const int32_t *send_idx, int64_t T, int32_t H, int32_t R,
                            void *out, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The expert layer in 8-bit floating point, and the norm in front of it.
+ *
+ * 8-bit tensors are e4m3 codes (one byte, finite range +-448, NaN but no
+ * infinity) with one scale per block: per 128 consecutive values of a row
+ * ([M,K]: scales [M, ceil(K/128)]), per 128 x 128 values of a weight
+ * ([E,N,K]: scales [E, ceil(N/128), ceil(K/128)]).  The value is code * scale.
+ * A scale is a power of two held as e8m0 (MOE_SCALE_E8M0: byte b stands for
+ * 2^(b-127), 255 for NaN) or any fp32 (MOE_SCALE_F32).
+ *
+ * The quantisers here (the norm's 8-bit output, moe_fp8_quantize_*) write
+ * e8m0: the smallest power of two s with amax <= 448 s, amax being the block's
+ * largest finite magnitude (s = 1 for a block of zeros; at least 2^-126).
+ * A power of two keeps every code's value exact in bf16 and the division by it
+ * exact, so a value is rounded once, to nearest even.  NaN and infinities
+ * become the NaN code.
+ *
+ * The layouts are dense row-major and the buffers device memory of the
+ * caller; calls are enqueued on `stream` without a host sync and allocate
+ * nothing.  Return codes as above (MOE_ERR_SHAPE: a size that is not a
+ * multiple of what the call asks for, or out of its range).
+ * ------------------------------------------------------------------------- */
+#define MOE_SCALE_E8M0 0
+#define MOE_SCALE_F32 1
+
+/*
+ * RMS norm with the residual's addition:
+ *   s = bf16(x + residual)             (s = x when residual is NULL)
+ *   inv = 1 / sqrt(mean_j s_j^2 + eps)
+ *   y_j = s_j inv weight_j
+ * x, residual [N,H], weight [H]: bf16.  Written: res [N,H] bf16 = s (given
+ * exactly when residual is); y [N,H] bf16 or NULL; y8 [N,H] e4m3 and y8_scale
+ * [N, ceil(H/128)] e8m0, or both NULL (at least one of y and y8); inv_rms [N]
+ * fp32 or NULL (the backward reads it).  res may be residual or x itself, and
+ * y may be x; no other buffers may overlap.  Sums are fp32; y is rounded once
+ * to each output type.  H a multiple of 8, at most 16384; eps >= 0; bf16 and
+ * e4m3 buffers 16-byte aligned.  One kernel launch.
+ */
+MOE_API int moe_add_rmsnorm(const void *x, const void *residual, const void *weight, int64_t N, int32_t H, float eps,
+                            void *res, void *y, void *y8, void *y8_scale, float *inv_rms, moe_stream_t stream);
+
+/*
+ * Its gradient, given dy [N,H] bf16 (of y), the forward's res (x when it had
+ * no residual), weight, inv_rms, and dres [N,H] bf16, the gradient that reaches
+ * res from the rest of the residual stream, or NULL for none:
+ *   c_t = (1/H) sum_j weight_j dy_tj res_tj
+ *   dx_tj = dres_tj + inv_t weight_j dy_tj - inv_t^3 c_t res_tj   (of x and of residual alike)
+ *   dweight_j = sum_t dy_tj res_tj inv_t
+ * dx [N,H] bf16 (may be dy or dres itself), dweight [H] fp32: both written
+ * whole (dweight = 0 for N = 0).  fp32 sums in a fixed order (no atomics).
+ * ws: 256-byte aligned, of at least the given size; its contents need no
+ * initialisation.  Two kernel launches.
+ */
+MOE_API size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t N, int32_t H);
+MOE_API int moe_add_rmsnorm_backward(const void *dy, const void *res, const void *weight, const float *inv_rms,
+                                     const void *dres, int64_t N, int32_t H, void *dx, float *dweight, void *ws,
+                                     size_t ws_bytes, moe_stream_t stream);
+
+/* x [M,K] bf16 -> q [M,K] e4m3, scale [M, ceil(K/128)] e8m0.  K a multiple of 16. */
+MOE_API int moe_fp8_quantize_rows(const void *x, int64_t M, int32_t K, void *q, void *scale, moe_stream_t stream);
+
+/*
+ * Weights w [E,K,N] bf16 (the layout of w1 [E,H,2I] and w2 [E,I,H]) -> q
+ * [E,N,K] e4m3, scale [E, ceil(N/128), ceil(K/128)] e8m0: the layout that the
+ * 8-bit products read, to be made once.  The order of the columns n stays
+ * (interleaved or concatenated gate and up).  K a multiple of 16, N of 8.
+ */
+MOE_API int moe_fp8_quantize_weight(const void *w, int32_t E, int32_t K, int32_t N, void *q, void *scale,
+                                    moe_stream_t stream);
+
+/*
+ * Product of 8-bit rows and an 8-bit weight, both scaled per block of 128:
+ *   out[m,n] = bf16( sum_k a[m,k] w[n,k] + bias[n] )
+ * a [M,K], w [N,K] e4m3 with their scales; bias [N] bf16 or NULL; out [M,N]
+ * bf16.  Each block of 128 along K is summed by the tensor cores and added in
+ * fp32 with its two scales; no long sum is held in less.  K a multiple of 16,
+ * N of 8; a, w, out 16-byte aligned.  err_word: device uint32 (MOE_DEVERR_*
+ * bits are OR-ed in, never cleared) or NULL.  One kernel launch.
+ */
+MOE_API int moe_fp8_linear(const void *a, const void *a_scale, int32_t a_scale_dtype, int64_t M, int32_t K,
+                           const void *w, const void *w_scale, int32_t w_scale_dtype, int32_t N, const void *bias,
+                           void *out, uint32_t *err_word, moe_stream_t stream);
+
+/*
+ * The same grouped by expert: for e < E and p in [expert_off[e], expert_off[e+1])
+ *   out[p,n] = bf16( sum_k a[row(p),k] w[e,n,k] + bias[e,n] )
+ * with row(p) = p (gather NULL, P = rows) or gather[p].  expert_off [E+1]
+ * int32 ascending (moe_meta_t.expert_frequency_offset), segments of any
+ * length, empty ones included; gather [P] int32 (moe_meta_t.x_gather_idx); w
+ * [E,N,K], bias [E,N].  Rows of out that no segment covers keep what they
+ * held.  Offsets are held inside [0,P]; a gathered row outside [0,rows)
+ * counts as zeros (rows >= 1 where P > 0).  Otherwise as moe_fp8_linear; E <= 1024.
+ */
+MOE_API int moe_fp8_grouped_linear(const void *a, const void *a_scale, int32_t a_scale_dtype, int64_t rows, int32_t K,
+                                   const int32_t *gather, int64_t P, const int32_t *expert_off, int32_t E,
+                                   const void *w, const void *w_scale, int32_t w_scale_dtype, int32_t N,
+                                   const void *bias, void *out, uint32_t *err_word, moe_stream_t stream);
+
+/*
+ * moe_nonexpand_routed_forward in 8 bits (inference): metadata, product up on
+ * the rows of x with bias and SwiGLU, h requantised to e4m3 (e8m0 scale per
+ * 128 columns, from the fp32 values), product down with bias, combine.
+ *   x [N,H] e4m3 + scales, w1 [E,2I,H], w2 [E,H,I] e4m3 + scales
+ *   (moe_fp8_quantize_weight of the bf16 weights), b1 [E,2I], b2 [E,H] bf16 or
+ *   NULL (b1 in w1's column order), out [N,H] bf16.
+ * routing, activation, gate_up_layout, meta_out and the workspace's rules as
+ * for the bf16 forward (moe_nonexpand_read_error reads its error word).  H and
+ * I multiples of 128.
+ */
+MOE_API size_t moe_fp8_forward_workspace_bytes(const moe_routing_t *routing, int32_t H, int32_t I, int32_t E);
+MOE_API int moe_fp8_forward(const void *x, const void *x_scale, int32_t x_scale_dtype, const moe_routing_t *routing,
+                            int32_t H, int32_t I, int32_t E, const void *w1, const void *w1_scale,
+                            int32_t w1_scale_dtype, const void *b1, const void *w2, const void *w2_scale,
+                            int32_t w2_scale_dtype, const void *b2, int32_t activation, int32_t gate_up_layout,
+                            void *out, const moe_meta_t *meta_out, void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Byte offsets of the workspace's internal arrays (for inspection and tests).
  * Offsets of arrays that the given sizes do not need are 0. */

@@ -65,6 +65,15 @@ EXPORTED = (
     "moe_ep_layout",
     "moe_ep_dispatch",
     "moe_ep_combine",
+    "moe_add_rmsnorm",
+    "moe_add_rmsnorm_backward_workspace_bytes",
+    "moe_add_rmsnorm_backward",
+    "moe_fp8_quantize_rows",
+    "moe_fp8_quantize_weight",
+    "moe_fp8_linear",
+    "moe_fp8_grouped_linear",
+    "moe_fp8_forward_workspace_bytes",
+    "moe_fp8_forward",
 )
 
 EP_MAX_RANKS = 32
@@ -74,6 +83,9 @@ ROUTER_TOPK_SOFTMAX = 1
 ROUTER_TOPK_SOFTMAX_RENORM = 2
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+
+SCALE_E8M0 = 0
+SCALE_F32 = 1
 
 
 class MoeMeta(ctypes.Structure):
@@ -189,6 +201,26 @@ def load() -> ctypes.CDLL:
     lib.moe_ep_dispatch.argtypes = [P, P, P, P, i64, i32, i32, i32, i32, ctypes.POINTER(MoeEpPeers), P]
     lib.moe_ep_combine.restype = ctypes.c_int
     lib.moe_ep_combine.argtypes = [ctypes.POINTER(MoeEpSources), P, i64, i32, i32, P, P]
+    f32 = ctypes.c_float
+    lib.moe_add_rmsnorm.restype = ctypes.c_int
+    lib.moe_add_rmsnorm.argtypes = [P, P, P, i64, i32, f32, P, P, P, P, P, P]
+    lib.moe_add_rmsnorm_backward_workspace_bytes.restype = sz
+    lib.moe_add_rmsnorm_backward_workspace_bytes.argtypes = [i64, i32]
+    lib.moe_add_rmsnorm_backward.restype = ctypes.c_int
+    lib.moe_add_rmsnorm_backward.argtypes = [P, P, P, P, P, i64, i32, P, P, P, sz, P]
+    lib.moe_fp8_quantize_rows.restype = ctypes.c_int
+    lib.moe_fp8_quantize_rows.argtypes = [P, i64, i32, P, P, P]
+    lib.moe_fp8_quantize_weight.restype = ctypes.c_int
+    lib.moe_fp8_quantize_weight.argtypes = [P, i32, i32, i32, P, P, P]
+    lib.moe_fp8_linear.restype = ctypes.c_int
+    lib.moe_fp8_linear.argtypes = [P, P, i32, i64, i32, P, P, i32, i32, P, P, P, P]
+    lib.moe_fp8_grouped_linear.restype = ctypes.c_int
+    lib.moe_fp8_grouped_linear.argtypes = [P, P, i32, i64, i32, P, i64, P, i32, P, P, i32, i32, P, P, P, P]
+    lib.moe_fp8_forward_workspace_bytes.restype = sz
+    lib.moe_fp8_forward_workspace_bytes.argtypes = [R, i32, i32, i32]
+    lib.moe_fp8_forward.restype = ctypes.c_int
+    lib.moe_fp8_forward.argtypes = [P, P, i32, R, i32, i32, i32, P, P, i32, P, P, P, i32, P, i32, i32, P,
+                                    ctypes.POINTER(MoeMeta), P, sz, P]
     lib.moe_nonexpand_strerror.restype = ctypes.c_char_p
     lib.moe_nonexpand_strerror.argtypes = [ctypes.c_int]
     _lib = lib
@@ -822,3 +854,283 @@ def routed_backward(dout: torch.Tensor, x: torch.Tensor, expert_idx: torch.Tenso
                                                 _ptr(g.get("db2")), g["dweights"].data_ptr(), ws.data_ptr(),
                                                 ws.numel(), _stream_handle(stream)), "moe_nonexpand_routed_backward")
     return g
+
+
+# ---------------------------------------------------------------------------
+# RMS norm with the residual's addition, and the layer in 8-bit floating point.
+#
+# 8-bit tensors are torch.float8_e4m3fn with one scale per block of 128 (rows
+# [M,K]: [M, ceil(K/128)]; weights [E,N,K]: [E, ceil(N/128), ceil(K/128)]), held
+# as torch.float8_e8m0fnu (powers of two, what the quantisers write) or float32.
+#
+# These calls run on the device of their tensors, whichever device is current,
+# and on ``stream`` (of that device) or that device's current stream; what they
+# allocate belongs to that stream.
+# ---------------------------------------------------------------------------
+
+_E4M3 = torch.float8_e4m3fn
+_E8M0 = torch.float8_e8m0fnu
+_SCALE_DTYPES = {torch.float8_e8m0fnu: SCALE_E8M0, torch.float32: SCALE_F32}
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _need_dim(t: torch.Tensor, name: str, dim: int):
+    if t.dim() != dim:
+        raise ValueError(f"{name}: expected {dim} dimensions, got shape {tuple(t.shape)}")
+
+
+def _need_scale(t: torch.Tensor, name: str, shape, device) -> int:
+    if t.dtype not in _SCALE_DTYPES:
+        raise TypeError(f"{name}: expected float8_e8m0fnu or float32, got {t.dtype}")
+    _need(t, name, t.dtype, shape, device)
+    return _SCALE_DTYPES[t.dtype]
+
+
+def _new(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A buffer that belongs to the stream the kernels run on."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _given(t: Optional[torch.Tensor], name: str, dtype, shape, device, stream) -> torch.Tensor:
+    """``t`` checked, or a new buffer."""
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    _need(t, name, dtype, shape, device)
+    return t
+
+
+def _call_on(device, stream: Optional[torch.cuda.Stream], name: str, *args):
+    """The entry point ``name`` on ``device``'s stream, which is its last argument."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: expected CUDA tensors, got {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, stream.cuda_stream), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream.cuda_stream), name)
+
+
+def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
+                eps: float = 1e-6, y: bool = True, fp8: bool = False, inv_rms: bool = False,
+                out: Optional[dict] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """RMS norm of x (+ residual) (moe_add_rmsnorm): s = bf16(x + residual),
+    y = s / sqrt(mean(s^2) + eps) * weight.
+
+    x, residual [N,H] and weight [H] bf16.  Returns a dict of what was asked
+    for: "res" (s, with a residual), "y" (bf16), "y8" and "y8_scale" (``fp8``:
+    e4m3 and e8m0 per 128 columns), "inv_rms" [N] (for add_rmsnorm_backward).
+    ``out`` may hold buffers for any of them; out["res"] may be the residual
+    itself."""
+    _need_dim(x, "x", 2)
+    N, H = x.shape
+    dev = x.device
+    _need(x, "x", torch.bfloat16, (N, H), dev)
+    _need(weight, "weight", torch.bfloat16, (H,), dev)
+    if not (y or fp8):
+        raise ValueError("add_rmsnorm: ask for y, fp8 or both")
+    out = out or {}
+    r = {}
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (N, H), dev)
+        r["res"] = _given(out.get("res"), "res", torch.bfloat16, (N, H), dev, stream)
+    if y:
+        r["y"] = _given(out.get("y"), "y", torch.bfloat16, (N, H), dev, stream)
+    if fp8:
+        r["y8"] = _given(out.get("y8"), "y8", _E4M3, (N, H), dev, stream)
+        r["y8_scale"] = _given(out.get("y8_scale"), "y8_scale", _E8M0, (N, _blocks(H)), dev, stream)
+    if inv_rms:
+        r["inv_rms"] = _given(out.get("inv_rms"), "inv_rms", torch.float32, (N,), dev, stream)
+    for k in out:
+        if k not in r:
+            raise ValueError(f"out: {k!r} is not written by this call")
+    _call_on(dev, stream, "moe_add_rmsnorm", x.data_ptr(), _ptr(residual), weight.data_ptr(), N, H, eps,
+             _ptr(r.get("res")), _ptr(r.get("y")), _ptr(r.get("y8")), _ptr(r.get("y8_scale")), _ptr(r.get("inv_rms")))
+    return r
+
+
+def add_rmsnorm_backward_workspace_bytes(N: int, H: int) -> int:
+    n = load().moe_add_rmsnorm_backward_workspace_bytes(N, H)
+    if n == 0:
+        raise MoeError(MOE_ERR_SHAPE, "moe_add_rmsnorm_backward_workspace_bytes")
+    return n
+
+
+def add_rmsnorm_backward(dy: torch.Tensor, res: torch.Tensor, weight: torch.Tensor, inv_rms: torch.Tensor, *,
+                         dres: Optional[torch.Tensor] = None, grads: Optional[dict] = None,
+                         ws: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """The gradient of add_rmsnorm (moe_add_rmsnorm_backward): dict(dx [N,H]
+    bf16, dweight [H] fp32).  ``res`` and ``inv_rms`` as the forward returned
+    them (res = x without a residual); ``dres`` is the gradient that reaches res
+    from the rest of the residual stream.  dx is the gradient of x and of the
+    residual alike.  ``grads`` may hold the two buffers."""
+    _need_dim(dy, "dy", 2)
+    N, H = dy.shape
+    dev = dy.device
+    _need(dy, "dy", torch.bfloat16, (N, H), dev)
+    _need(res, "res", torch.bfloat16, (N, H), dev)
+    _need(weight, "weight", torch.bfloat16, (H,), dev)
+    _need(inv_rms, "inv_rms", torch.float32, (N,), dev)
+    if dres is not None:
+        _need(dres, "dres", torch.bfloat16, (N, H), dev)
+    grads = grads or {}
+    r = dict(dx=_given(grads.get("dx"), "dx", torch.bfloat16, (N, H), dev, stream),
+             dweight=_given(grads.get("dweight"), "dweight", torch.float32, (H,), dev, stream))
+    if ws is None:
+        ws = _new((add_rmsnorm_backward_workspace_bytes(N, H),), torch.uint8, dev, stream)
+    _need(ws, "ws", torch.uint8, (ws.numel(),), dev)
+    _call_on(dev, stream, "moe_add_rmsnorm_backward", dy.data_ptr(), res.data_ptr(), weight.data_ptr(),
+             inv_rms.data_ptr(), _ptr(dres), N, H, r["dx"].data_ptr(), r["dweight"].data_ptr(), ws.data_ptr(), ws.numel())
+    return r
+
+
+def quantize_rows_fp8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None):
+    """x [M,K] bf16 -> (q [M,K] e4m3, scale [M, ceil(K/128)] e8m0) (moe_fp8_quantize_rows)."""
+    _need_dim(x, "x", 2)
+    M, K = x.shape
+    dev = x.device
+    _need(x, "x", torch.bfloat16, (M, K), dev)
+    q = _given(q, "q", _E4M3, (M, K), dev, stream)
+    scale = _given(scale, "scale", _E8M0, (M, _blocks(K)), dev, stream)
+    _call_on(dev, stream, "moe_fp8_quantize_rows", x.data_ptr(), M, K, q.data_ptr(), scale.data_ptr())
+    return q, scale
+
+
+def quantize_weight_fp8(w: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None):
+    """w [E,K,N] (or [K,N]) bf16 -> (q [E,N,K] e4m3, scale [E, ceil(N/128),
+    ceil(K/128)] e8m0), the layout of the 8-bit products (moe_fp8_quantize_weight)."""
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w: expected [E,K,N] or [K,N], got shape {tuple(w.shape)}")
+    lead = tuple(w.shape[:-2])
+    K, N = w.shape[-2:]
+    dev = w.device
+    _need(w, "w", torch.bfloat16, w.shape, dev)
+    q = _given(q, "q", _E4M3, lead + (N, K), dev, stream)
+    scale = _given(scale, "scale", _E8M0, lead + (_blocks(N), _blocks(K)), dev, stream)
+    _call_on(dev, stream, "moe_fp8_quantize_weight", w.data_ptr(), lead[0] if lead else 1, K, N, q.data_ptr(),
+             scale.data_ptr())
+    return q, scale
+
+
+def linear_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+               bias: Optional[torch.Tensor] = None, *, out: Optional[torch.Tensor] = None,
+               err: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """out [M,N] bf16 = a [M,K] . w [N,K]^T + bias [N], a and w e4m3 with
+    scales per block of 128 (moe_fp8_linear).  ``err``: int32 [1], collects
+    device error bits."""
+    _need_dim(a, "a", 2)
+    _need_dim(w, "w", 2)
+    M, K = a.shape
+    N = w.shape[0]
+    dev = a.device
+    _need(a, "a", _E4M3, (M, K), dev)
+    _need(w, "w", _E4M3, (N, K), dev)
+    sa = _need_scale(a_scale, "a_scale", (M, _blocks(K)), dev)
+    sw = _need_scale(w_scale, "w_scale", (_blocks(N), _blocks(K)), dev)
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, (N,), dev)
+    if err is not None:
+        _need(err, "err", torch.int32, (1,), dev)
+    out = _given(out, "out", torch.bfloat16, (M, N), dev, stream)
+    _call_on(dev, stream, "moe_fp8_linear", a.data_ptr(), a_scale.data_ptr(), sa, M, K, w.data_ptr(),
+             w_scale.data_ptr(), sw, N, _ptr(bias), out.data_ptr(), _ptr(err))
+    return out
+
+
+def grouped_linear_fp8(a: torch.Tensor, a_scale: torch.Tensor, expert_off: torch.Tensor, w: torch.Tensor,
+                       w_scale: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+                       gather: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       err: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """out[p] bf16 = a[row(p)] . w[e]^T + bias[e] for the rows p of expert e's
+    segment [expert_off[e], expert_off[e+1]) (moe_fp8_grouped_linear).
+
+    a [rows,K], w [E,N,K] e4m3 with scales per block of 128, expert_off [E+1]
+    int32, gather [P] int32 (row(p) = gather[p]) or None (row(p) = p, P = rows).
+    Rows of ``out`` behind the last segment are not written."""
+    _need_dim(a, "a", 2)
+    _need_dim(w, "w", 3)
+    rows, K = a.shape
+    E, N, _ = w.shape
+    dev = a.device
+    _need(a, "a", _E4M3, (rows, K), dev)
+    _need(w, "w", _E4M3, (E, N, K), dev)
+    sa = _need_scale(a_scale, "a_scale", (rows, _blocks(K)), dev)
+    sw = _need_scale(w_scale, "w_scale", (E, _blocks(N), _blocks(K)), dev)
+    _need(expert_off, "expert_off", torch.int32, (E + 1,), dev)
+    P = rows
+    if gather is not None:
+        P = gather.numel()
+        _need(gather, "gather", torch.int32, (P,), dev)
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, (E, N), dev)
+    if err is not None:
+        _need(err, "err", torch.int32, (1,), dev)
+    out = _given(out, "out", torch.bfloat16, (P, N), dev, stream)
+    if P > 0:
+        _call_on(dev, stream, "moe_fp8_grouped_linear", a.data_ptr(), a_scale.data_ptr(), sa, rows, K, _ptr(gather), P,
+                 expert_off.data_ptr(), E, w.data_ptr(), w_scale.data_ptr(), sw, N, _ptr(bias), out.data_ptr(),
+                 _ptr(err))
+    return out
+
+
+def fp8_workspace_bytes(r: MoeRouting, H: int, I: int, E: int) -> int:
+    n = load().moe_fp8_forward_workspace_bytes(ctypes.byref(r), H, I, E)
+    if n == 0:
+        raise MoeError(MOE_ERR_ARG, "moe_fp8_forward_workspace_bytes")
+    return n
+
+
+def forward_fp8(x: torch.Tensor, x_scale: torch.Tensor, expert_idx: torch.Tensor, weights: torch.Tensor,
+                w1: torch.Tensor, w1_scale: torch.Tensor, w2: torch.Tensor, w2_scale: torch.Tensor,
+                b1: Optional[torch.Tensor] = None, b2: Optional[torch.Tensor] = None, *,
+                token_idx: Optional[torch.Tensor] = None, layout: int = LAYOUT_INTERLEAVED, total_pairs: int = -1,
+                out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, meta: Optional[dict] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The expert layer's forward in 8 bits (moe_fp8_forward), for either
+    routing layout (see ``routing``): out [N,H] bf16.
+
+    x [N,H], w1 [E,2I,H], w2 [E,H,I] e4m3 with scales per block of 128 (x from
+    add_rmsnorm(fp8=True) or quantize_rows_fp8, the weights from
+    quantize_weight_fp8), b1 [E,2I] / b2 [E,H] bf16 or None, ws of
+    fp8_workspace_bytes."""
+    _need_dim(x, "x", 2)
+    _need_dim(w1, "w1", 3)
+    N, H = x.shape
+    E, I2, _ = w1.shape
+    I = I2 // 2
+    dev = x.device
+    _need(x, "x", _E4M3, (N, H), dev)
+    _need(w1, "w1", _E4M3, (E, 2 * I, H), dev)
+    _need(w2, "w2", _E4M3, (E, H, I), dev)
+    sx = _need_scale(x_scale, "x_scale", (N, _blocks(H)), dev)
+    s1 = _need_scale(w1_scale, "w1_scale", (E, _blocks(2 * I), _blocks(H)), dev)
+    s2 = _need_scale(w2_scale, "w2_scale", (E, _blocks(H), _blocks(I)), dev)
+    if b1 is not None:
+        _need(b1, "b1", torch.bfloat16, (E, 2 * I), dev)
+    if b2 is not None:
+        _need(b2, "b2", torch.bfloat16, (E, H), dev)
+    if expert_idx.device != dev:
+        raise ValueError(f"expert_idx: expected device {dev}, got {expert_idx.device}")
+    r = routing(expert_idx, weights, token_idx=token_idx, N=N, total_pairs=total_pairs)
+    out = _given(out, "out", torch.bfloat16, (N, H), dev, stream)
+    if ws is None:
+        ws = _new((fp8_workspace_bytes(r, H, I, E),), torch.uint8, dev, stream)
+    _need(ws, "ws", torch.uint8, (ws.numel(),), dev)
+    m = _meta_struct(meta) if meta is not None else None
+    _call_on(dev, stream, "moe_fp8_forward", x.data_ptr(), x_scale.data_ptr(), sx, ctypes.byref(r), H, I, E,
+             w1.data_ptr(), w1_scale.data_ptr(), s1, _ptr(b1), w2.data_ptr(), w2_scale.data_ptr(), s2, _ptr(b2),
+             ACT_SWIGLU, layout, out.data_ptr(), ctypes.byref(m) if m is not None else None, ws.data_ptr(), ws.numel())
+    return out

@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "ep.cuh"
+#include "fp8.cuh"
 
 
 namespace moe {
@@ -706,7 +707,135 @@ int backward_impl(const void *dout, const void *x, const Routing &r, int32_t H, 
     return MOE_OK;
 }
 
+// ---------------------------------------------------------------------------
+// The forward in 8 bits: metadata, block-scaled grouped product up with SwiGLU
+// and requantised h, product down, combine.
+// ---------------------------------------------------------------------------
+struct Fp8Layout {
+    moe_ws_layout_t meta;  // header, tables and metadata at the workspace's start
+    size_t h, h_scale, y, y_scale, total;
+};
+
+Fp8Layout fp8_layout(const Routing &r, int32_t H, int32_t I, int32_t E) {
+    Fp8Layout l;
+    l.meta = compute_layout_nk(r.N, 0, 0, E, r.NK, r.p_cap);
+    const size_t pc = (size_t)r.p_cap;
+    size_t o = align_up(l.meta.total, 1024);
+    l.h = o;
+    o = align_up(o + pc * I, 1024);
+    l.h_scale = o;
+    o = align_up(o + pc * (I / kScaleBlock), 1024);
+    l.y = o;
+    o = align_up(o + pc * H * 2, 1024);
+    l.y_scale = o;
+    o = align_up(o + pc * (H / kYBlock), 1024);
+    l.total = o;
+    return l;
+}
+
+int check_fp8_dense(int32_t H, int32_t I) {
+    if (H <= 0 || I <= 0 || H % kScaleBlock != 0 || I % kScaleBlock != 0 || I > (1 << 28) || H > (1 << 28))
+        return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+int fp8_forward_impl(const void *x, const void *x_scale, int32_t x_sd, const Routing &r, int32_t H, int32_t I,
+                     int32_t E, const void *w1, const void *w1_scale, int32_t w1_sd, const void *b1, const void *w2,
+                     const void *w2_scale, int32_t w2_sd, const void *b2, int32_t activation, int32_t layout_kind,
+                     void *out, const moe_meta_t *meta_out, void *ws, size_t ws_bytes, cudaStream_t s) {
+    auto sd_ok = [](int32_t d) { return d == MOE_SCALE_E8M0 || d == MOE_SCALE_F32; };
+    auto sc_ok = [](const void *p, int32_t d) { return d == MOE_SCALE_E8M0 || aligned(p, 4); };
+    if ((r.N > 0 && (!x || !x_scale || !out)) || !w1 || !w1_scale || !w2 || !w2_scale) return MOE_ERR_ARG;
+    if (activation != MOE_ACT_SWIGLU || !sd_ok(x_sd) || !sd_ok(w1_sd) || !sd_ok(w2_sd)) return MOE_ERR_ARG;
+    if (layout_kind != MOE_LAYOUT_INTERLEAVED && layout_kind != MOE_LAYOUT_CONCATENATED) return MOE_ERR_ARG;
+    if (meta_out && !meta_complete(meta_out)) return MOE_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(out, 16) || !aligned(b1, 2) ||
+        !aligned(b2, 2) || !sc_ok(x_scale, x_sd) || !sc_ok(w1_scale, w1_sd) || !sc_ok(w2_scale, w2_sd))
+        return MOE_ERR_ARG;
+    int st = check_fp8_dense(H, I);
+    if (st) return st;
+    const Fp8Layout l = fp8_layout(r, H, I, E);
+    if (!ws || !aligned(ws, kAlign) || ws_bytes < l.total) return MOE_ERR_WS;
+    DeviceInfo dev;
+    st = device_info(&dev);
+    if (st) return st;
+
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    const moe_meta_t meta = meta_out ? *meta_out : ws_meta(l.meta, w);
+    const MetaArgs ma = meta_args(r, E, l.meta, w, meta);
+    if (launch_meta(ma, s) != cudaSuccess) return MOE_ERR_CUDA;
+    if (r.p_cap > 0) {
+        Fp8GemmArgs g;
+        memset(&g, 0, sizeof g);
+        g.expert_off = meta.expert_frequency_offset;
+        g.hdr = ma.hdr;
+        g.err = &ma.hdr->err;
+        g.P = r.p_cap;
+        g.E = E;
+        Fp8GemmArgs up = g;
+        up.w = static_cast<const uint8_t *>(w1);
+        up.a = static_cast<const uint8_t *>(x);
+        up.a_scale = x_scale;
+        up.w_scale = w1_scale;
+        up.a_f32 = x_sd == MOE_SCALE_F32;
+        up.w_f32 = w1_sd == MOE_SCALE_F32;
+        up.gather = meta.x_gather_idx;
+        up.bias = static_cast<const __nv_bfloat16 *>(b1);
+        up.out = w + l.h;
+        up.out_scale = w + l.h_scale;
+        up.rows = r.N;
+        up.K = H;
+        up.N = 2 * I;
+        up.nk = scale_blocks(H);
+        up.layout = layout_kind;
+        if (launch_fp8_gemm(kFp8SwiGlu, up, dev.sms, s) != cudaSuccess) return MOE_ERR_CUDA;
+        Fp8GemmArgs dn = g;
+        dn.w = static_cast<const uint8_t *>(w2);
+        dn.a = w + l.h;
+        dn.a_scale = w + l.h_scale;
+        dn.w_scale = w2_scale;
+        dn.w_f32 = w2_sd == MOE_SCALE_F32;
+        dn.bias = static_cast<const __nv_bfloat16 *>(b2);
+        dn.out = w + l.y;
+        dn.out_scale = w + l.y_scale;
+        dn.rows = r.p_cap;
+        dn.K = I;
+        dn.N = H;
+        dn.nk = scale_blocks(I);
+        if (launch_fp8_gemm(kFp8Y16, dn, dev.sms, s) != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    if (launch_combine(w + l.y, reinterpret_cast<const int8_t *>(w + l.y_scale), meta.token_offset,
+                       meta.s_reverse_scatter_idx, meta.scores, r.N, H, static_cast<__nv_bfloat16 *>(out), ma.hdr,
+                       dev.sms, s, false) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return MOE_OK;
+}
+
 }  // namespace
+
+int current_device_sms(int *sms) {
+    DeviceInfo d;
+    const int st = device_info(&d);
+    *sms = d.sms;
+    return st;
+}
+
+bool make_map_u8(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
+                 const uint32_t *box) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    cuuint64_t d[3], st[2];
+    cuuint32_t b[3], estr[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(ptr), d, st, b, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -1010,6 +1139,27 @@ extern "C" MOE_API int moe_ep_combine(const moe_ep_sources_t *src, const int32_t
                : MOE_ERR_CUDA;
 }
 
+extern "C" MOE_API size_t moe_fp8_forward_workspace_bytes(const moe_routing_t *routing, int32_t H, int32_t I,
+                                                          int32_t E) {
+    Routing r;
+    if (routing_from_desc(routing, E, &r) || check_fp8_dense(H, I)) return 0;
+    return fp8_layout(r, H, I, E).total;
+}
+
+extern "C" MOE_API int moe_fp8_forward(const void *x, const void *x_scale, int32_t x_scale_dtype,
+                                       const moe_routing_t *routing, int32_t H, int32_t I, int32_t E, const void *w1,
+                                       const void *w1_scale, int32_t w1_scale_dtype, const void *b1, const void *w2,
+                                       const void *w2_scale, int32_t w2_scale_dtype, const void *b2,
+                                       int32_t activation, int32_t gate_up_layout, void *out,
+                                       const moe_meta_t *meta_out, void *ws, size_t ws_bytes, moe_stream_t stream) {
+    Routing r;
+    const int st = routing_from_desc(routing, E, &r);
+    if (st) return st;
+    return fp8_forward_impl(x, x_scale, x_scale_dtype, r, H, I, E, w1, w1_scale, w1_scale_dtype, b1, w2, w2_scale,
+                            w2_scale_dtype, b2, activation, gate_up_layout, out, meta_out, ws, ws_bytes,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
 extern "C" MOE_API int moe_nonexpand_read_error(const void *ws, moe_stream_t stream, uint32_t *err_word) {
     if (!ws || !err_word) return MOE_ERR_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1025,7 +1175,7 @@ extern "C" MOE_API const char *moe_nonexpand_strerror(int status) {
     switch (status) {
         case MOE_OK: return "ok";
         case MOE_ERR_ARG: return "invalid argument";
-        case MOE_ERR_SHAPE: return "unsupported shape (H and I must be multiples of 64)";
+        case MOE_ERR_SHAPE: return "unsupported shape (a size is out of range or no multiple of what the call needs)";
         case MOE_ERR_WS: return "workspace missing, misaligned or too small";
         case MOE_ERR_CUDA: return "CUDA runtime or launch failure";
         case MOE_ERR_DEVICE: return "current device is not an sm_100 (B200-class) GPU";
