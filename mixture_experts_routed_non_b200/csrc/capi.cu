@@ -820,6 +820,10 @@ int current_device_sms(int *sms) {
     return st;
 }
 
+bool make_map_16(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows) {
+    return make_map_2d(m, ptr, cols, rows, box_cols, box_rows);
+}
+
 bool make_map_u8(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
                  const uint32_t *box) {
     EncodeTiledFn f = encode_fn();
