@@ -41,7 +41,8 @@ struct Fp8GemmArgs {
 };
 
 cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);       // picks the kernel
-cudaError_t launch_fp8_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);  // 256-row tiles
+cudaError_t launch_fp8_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);     // 256-row tiles, any scales
+cudaError_t launch_fp8_mx_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);  // 256-row tiles, e8m0
 
 struct NormArgs {
     const __nv_bfloat16 *x, *residual, *weight;
@@ -101,6 +102,22 @@ __device__ __forceinline__ float load_scale(const void *p, int f32, size_t i) {
     return __uint_as_float(b == 0 ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
 }
 
+// The same in two steps, for loads that should be in flight together: the raw
+// bits of n scales from index i on, and their values.
+template <int n>
+__device__ __forceinline__ void load_scale_bits(const void *p, int f32, size_t i, int last, uint32_t (&raw)[n]) {
+    if (f32) {
+#pragma unroll
+        for (int k = 0; k < n; ++k) raw[k] = __ldg(static_cast<const uint32_t *>(p) + i + min(k, last));
+    } else {
+#pragma unroll
+        for (int k = 0; k < n; ++k) raw[k] = __ldg(static_cast<const uint8_t *>(p) + i + min(k, last));
+    }
+}
+__device__ __forceinline__ float scale_of_bits(uint32_t raw, int f32) {
+    return __uint_as_float(f32 ? raw : raw == 0 ? 0x00400000u : raw == 255u ? 0x7FC00000u : raw << 23);
+}
+
 // Infinities become NaN (e4m3 has no infinity, and the conversion would
 // saturate them); every other value is unchanged.
 __device__ __forceinline__ float inf_to_nan(float v) { return fmaf(v, 0.0f, v); }
@@ -130,6 +147,13 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
 // Instruction descriptor, kind::f8f6f4: fp32 accumulate, A and B e4m3 (format 0), both K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
     return (1u << 4) | ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 #endif  // __CUDACC__

@@ -1,0 +1,435 @@
+// Block-scaled e4m3 products for long segments with power-of-two (e8m0) scales on
+// both sides: the computation of fp8_gemm_sm100.cu on CTA pairs (tile:
+// fp8_pair.cuh) with the scales applied by the tensor cores.
+//
+// tcgen05.mma.kind::mxf8f6f4.block_scale multiplies each product by an e8m0 scale
+// of its row of `a` and one of its weight row, per 32 values of K, and sums into
+// an fp32 accumulator; a scale per 128 values is four equal ones.  The whole K of
+// a tile stays in one TMEM accumulator, and nothing but the two operands and
+// their scales moves per block.
+//
+// Scales in TMEM (one byte of a 32-bit word per K step of 32, all four the same
+// here): row 32 c + l of a 128-row operand in lane l of column c, repeated in each
+// lane quarter -- four columns for a CTA's 128 rows of `a`, eight for the tile's
+// 256 weight rows, which both CTAs hold.  Four scale warps per CTA, one per lane
+// quarter, load the scale bytes ahead and store these columns for each stage.
+//
+// TMEM: the accumulator (256 columns) and a 16-column scale slot per stage.  A
+// second accumulator does not fit beside them, so the epilogue first takes the
+// whole accumulator into registers (64 per thread) and hands it back; conversion
+// and stores run behind the next tile's MMAs.
+//
+// Warp roles: 0 = TMA producer, 1 = TMEM allocator and MMA issuer (even CTA), 2 =
+// gather relay (fp8_gemm_pair_sm100.cu), 4-7 = scales, 8-23 = epilogue, 24-27 =
+// row gather (gathered rows only).  Registers are moved to the epilogue warps
+// (setmaxnreg: with gathered rows 4 x 96 + 3 x 40 per thread of the seven
+// warpgroups, the 7 x 72 of the launch; else 4 x 96 + 2 x 48 = 6 x 80).  Every wait
+// is bounded (common.cuh).
+#include "fp8_pair.cuh"
+
+namespace moe {
+namespace {
+
+// registers per thread of the launch, of the epilogue warpgroups and of the others
+__host__ __device__ constexpr int x_threads(bool gather) { return gather ? 896 : 768; }
+__host__ __device__ constexpr int x_other_regs(bool gather) { return gather ? 40 : 48; }
+constexpr int kXEpiRegs = 96;
+static_assert(4 * kXEpiRegs + 3 * x_other_regs(true) == 7 * 72 && 4 * kXEpiRegs + 2 * x_other_regs(false) == 6 * 80,
+              "the warpgroups' registers are those of the launch");
+constexpr uint32_t kXScaleCols = 16;  // TMEM columns of a stage's scales: `a` at 0, weights at 8
+
+template <int kMode>
+struct XCfg {
+    // 16-bit outputs pass through 64 KB of store buffers; the e4m3 rows of SwiGLU are whole
+    // sectors per thread and are stored directly
+    static constexpr int kStages = kMode == kFp8SwiGlu ? 6 : 4;
+    static constexpr int kBars = 3 * kStages + 3;
+    static constexpr size_t kStoreOff = (size_t)kStages * kPStage;
+    static constexpr size_t kMaxOff = kStoreOff + (kMode == kFp8SwiGlu ? 0 : kPEpiWarps * kPStore);  // [4][128]
+    static constexpr size_t kBarOff = kMaxOff + 4 * 128 * 4;
+    static constexpr size_t kMiscOff = kBarOff + 8 * kBars + 8;
+    static constexpr size_t kTableOff = kMiscOff + 16;
+    static constexpr size_t kSmem = 1024 + kTableOff + 2 * (kMaxExperts + 1) * 4;
+    static_assert(kSmem <= 232448, "shared memory of one CTA (227 KB)");
+    static_assert(kPN + kStages * kXScaleCols <= kPTmem, "TMEM columns");
+};
+
+// D[tmem] (+)= (A * scales) (B * scales), e4m3 in, one e8m0 scale per 32 K of each row, K = 32.
+__device__ __forceinline__ void umma_mx_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor, kind::mxf8f6f4: A and B e4m3 (format 0), both K-major, e8m0 scales
+// (bit 23), byte 0 of the scale words (both scale ids 0), M x N.
+__host__ __device__ constexpr uint32_t idesc_mx_e4m3(int M, int N) {
+    return ((static_cast<uint32_t>(N) >> 3) << 17) | (1u << 23) | ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+// 32 lanes x 4 (8) 32-bit TMEM columns from registers.
+__device__ __forceinline__ void tmem_st_x4(uint32_t taddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r0), "r"(r1),
+                 "r"(r2), "r"(r3)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The e8m0 bytes of blocks kb .. kb + 3 (the last block repeated behind the end) in one word.
+__device__ __forceinline__ uint32_t load_e8m0_x4(const uint8_t *p, size_t i, int last) {
+    const uint8_t *q = p + i;
+    if (last >= 3 && (reinterpret_cast<uintptr_t>(q) & 3) == 0) return __ldg(reinterpret_cast<const uint32_t *>(q));
+    const uint32_t b0 = __ldg(q), b1 = __ldg(q + min(1, last)), b2 = __ldg(q + min(2, last)), b3 = __ldg(q + min(3, last));
+    return b0 | b1 << 8 | b2 << 16 | b3 << 24;
+}
+
+template <int kMode, bool kGather>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 1)
+    fp8_mx_pair_kernel(const __grid_constant__ Fp8GemmArgs a) {
+    using C = XCfg<kMode>;
+    constexpr int kPStages = C::kStages, kPThreads = x_threads(kGather);
+    extern __shared__ uint8_t smem_raw[];
+    // uniform for both CTAs of the pair: they return together
+    if (a.hdr && *(volatile const uint32_t *)&a.hdr->abort) return;
+
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *base_ptr = smem_raw + (base - raw);
+    const uint32_t bars = base + (uint32_t)C::kBarOff;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (kPStages + s); };
+    auto gfull_bar = [&](int s) { return bars + 8u * (2 * kPStages + s); };
+    const uint32_t tfull_bar = bars + 8u * (3 * kPStages);
+    const uint32_t tempty_bar = tfull_bar + 8u, drain_bar = tfull_bar + 16u;
+    uint32_t *misc = reinterpret_cast<uint32_t *>(base_ptr + C::kMiscOff);
+    int *off_s = reinterpret_cast<int *>(base_ptr + C::kTableOff);
+    int *pre_s = off_s + (kMaxExperts + 1);
+    float *max_s = reinterpret_cast<float *>(base_ptr + C::kMaxOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int E = a.E;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPStages; ++s) {
+            // even CTA: the producer's arrive (+ both CTAs' TMA bytes), both CTAs' scale warps and,
+            // with gathered rows, both CTAs' relays
+            mbar_init(full_bar(s), 1 + 8 + (kGather ? 2 : 0));
+            mbar_init(empty_bar(s), 1);
+            mbar_init(gfull_bar(s), kPGather);
+        }
+        mbar_init(tfull_bar, 1);
+        mbar_init(tempty_bar, 2 * kPEpiWarps);
+        mbar_init(drain_bar, 1);
+        misc[1] = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 32) {
+        tma_prefetch_desc(&a.tmap_w);
+        if (!kGather) tma_prefetch_desc(&a.tmap_a);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&misc[0]), kPTmem);
+        tmem_relinquish_pair();
+    }
+    load_offsets(a, off_s, kPThreads);
+    __syncthreads();
+    if (warp == 0) prefix_pieces(off_s, pre_s, E, kPM, lane);
+    tc_fence_before();
+    cluster_sync_all();  // barriers of both CTAs initialised before any remote arrive
+    tc_fence_after();
+
+    const uint32_t tmem_base = misc[0];
+    volatile uint32_t *abort = &misc[1];
+    const int nk = a.nk;
+    const bool concat = kMode == kFp8SwiGlu && a.layout == MOE_LAYOUT_CONCATENATED;
+    const PTiles list{off_s, pre_s, E, a.N, (a.N + kPN - 1) / kPN, concat};
+    const long long tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
+
+    if (warp < 4) {
+        regs_dec<x_other_regs(kGather)>();
+        if (warp == 0 && lane == 0) {
+            // -------------------------------------------------------- producer
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, issued_parity = 0;
+            bool ok = true;
+            for (long long u = t0; ok && u < tiles; u += dt) {
+                const PTile t = list.at(u);
+                const int wr = list.wrow(t.nt, (int)rank), ar = t.m0 + 128 * (int)rank;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    // both CTAs' TMA bytes land on the even CTA's barrier
+                    if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), kGather ? 2 * kPHalf : 4 * kPHalf);
+                    const uint32_t fb = mapa_shared(full_bar(stage), 0), dst = base + stage * kPStage;
+                    tma_load_3d_pair(dst + kPHalf, &a.tmap_w, fb, kb * kPK, wr, t.e);
+                    if (!kGather) tma_load_2d_pair(dst, &a.tmap_a, fb, kb * kPK, ar);
+                    issued |= 1u << stage;
+                    issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                    if (++stage == kPStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // the even CTA's full barriers count both CTAs' bytes: wait for every phase this
+            // CTA issued before the CTA may exit
+            if (rank == 0)
+                for (int s = 0; s < kPStages; ++s)
+                    if ((issued & (1u << s)) && !mbar_wait_timed(full_bar(s), (issued_parity >> s) & 1u)) *abort = 1u;
+        } else if (warp == 1 && rank == 0) {
+            // ------------------------------------------------------ MMA issuer
+            int stage = 0;
+            uint32_t phase = 0, tphase = 0;
+            bool ok = true;
+            constexpr uint32_t idesc = idesc_mx_e4m3(kPM, kPN);
+            // operand descriptors: K-major, 128-byte rows, 8-row atoms 1024 B apart; stages and K
+            // steps only move the start address (16-byte units, below 2^14), so the issue loop adds
+            const uint64_t desc0 = smem_desc_sw128(base, 16, 1024);
+            const bool leader = elect_one();
+            for (long long u = t0; ok && u < tiles; u += dt, tphase ^= 1u) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(tempty_bar, tphase ^ 1u, abort));
+                for (int kb = 0; ok && kb < nk; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t da = desc0 + (uint32_t)stage * (kPStage >> 4), db = da + (kPHalf >> 4);
+                    const uint32_t sf = tmem_base + kPN + (uint32_t)stage * kXScaleCols;
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_mx_pair(tmem_base, da + 2 * kk, db + 2 * kk, idesc, sf, sf + 8, (kb | kk) != 0 ? 1u : 0u);
+                        umma_commit_pair_mc(empty_bar(stage), 0x3);
+                        if (kb == nk - 1) umma_commit_pair_mc(tfull_bar, 0x3);
+                    }
+                    __syncwarp();
+                    if (++stage == kPStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // all pair MMAs issued here complete before TMEM is freed
+            if (leader) {
+                umma_commit_pair(drain_bar);
+                if (!mbar_wait_timed(drain_bar, 0)) *abort = 1u;
+            }
+        } else if (kGather && warp == 2 && lane == 0) {
+            // ------------------------------------------------------ gather relay
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (long long u = t0; ok && u < tiles; u += dt)
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!mbar_wait_bounded(gfull_bar(stage), phase, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive_cluster(mapa_shared(full_bar(stage), 0));
+                    if (++stage == kPStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        regs_dec<x_other_regs(kGather)>();
+        // ------------------------------------------------------------ scales
+        const int nb = (a.N + 127) / 128;
+        const uint8_t *as = static_cast<const uint8_t *>(a.a_scale), *ws = static_cast<const uint8_t *>(a.w_scale);
+        const uint32_t sf0 = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + kPN;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (long long u = t0; ok && u < tiles; u += dt) {
+            const PTile t = list.at(u);
+            int srow[4];  // rows of `a`; -1: past the segment or outside `a` (their codes are zeros or never used)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int p = t.m0 + (int)rank * 128 + 32 * i + lane;
+                srow[i] = p < t.m_end ? (kGather ? __ldg(a.gather + p) : p) : -1;
+                if (srow[i] >= a.rows) srow[i] = -1;
+            }
+            size_t wi[2];  // (a half past the end of N has no scales: its columns are never stored)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) wi[h] = ((size_t)t.e * nb + min(list.wrow(t.nt, h) / 128, nb - 1)) * nk;
+            for (int kb = 0; ok && kb < nk; kb += 4) {
+                uint32_t ra[4], rw[2];
+                const int last = nk - 1 - kb;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ra[i] = srow[i] >= 0 ? load_e8m0_x4(as, (size_t)srow[i] * nk + kb, last) : 0x7F7F7F7Fu;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) rw[h] = load_e8m0_x4(ws, wi[h] + kb, last);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k > last) break;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
+                    if (!ok) break;
+                    const uint32_t sel = 0x1111u * (uint32_t)k;  // byte k four times
+                    const uint32_t sf = sf0 + (uint32_t)stage * kXScaleCols;
+                    const uint32_t w0 = __byte_perm(rw[0], 0, sel), w1 = __byte_perm(rw[1], 0, sel);
+                    tc_fence_after();
+                    tmem_st_x4(sf, __byte_perm(ra[0], 0, sel), __byte_perm(ra[1], 0, sel), __byte_perm(ra[2], 0, sel),
+                               __byte_perm(ra[3], 0, sel));
+                    tmem_st_x4(sf + 8, w0, w0, w0, w0);
+                    tmem_st_x4(sf + 12, w1, w1, w1, w1);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(full_bar(stage), 0));
+                    if (++stage == kPStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp < 24) {
+        regs_inc<kXEpiRegs>();
+        // ------------------------------------------------------------ epilogue
+        const int q4 = warp & 3, cq = (warp - 8) >> 2;
+        const uint32_t buf = base + (uint32_t)C::kStoreOff + (uint32_t)(warp - 8) * kPStore;
+        const uint32_t tempty0 = mapa_shared(tempty_bar, 0);
+        // the warp's two 32-column chunks of the accumulator: its own quarter, or (concatenated
+        // SwiGLU) one of the gates and the matching one of the ups
+        const int c0 = concat ? 32 * cq : 64 * cq, c1 = concat ? 128 + 32 * cq : 64 * cq + 32;
+        const uint32_t tb = tmem_base + ((uint32_t)(32 * q4) << 16);
+        uint32_t tphase = 0;
+        // a wait that gives up raises the abort flag; the warp then runs on over whatever is there
+        // (later waits give up at once), meets the named barriers, and stores nothing
+        for (long long u = t0; u < tiles; u += dt, tphase ^= 1u) {
+            const PTile t = list.at(u);
+            mbar_wait_bounded(tfull_bar, tphase, abort);
+            __syncwarp();
+            tc_fence_after();
+            uint32_t v0[32], v1[32];
+            tmem_ld_32x32b_x32(tb + c0, v0);
+            tmem_ld_32x32b_x32(tb + c1, v1);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0);
+            float acc[64];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                acc[j] = __uint_as_float(v0[j]);
+                acc[32 + j] = __uint_as_float(v1[j]);
+            }
+            pair_output<kMode>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s, *abort == 0);
+        }
+        if (lane == 0) bulk_wait0();  // this warp's stores are complete
+    } else {
+        regs_dec<x_other_regs(kGather)>();
+        if (kGather) {
+            // --------------------------------------------------- row gather
+            // thread g: 16-byte piece (g & 7) of rows (g >> 3) + 16 i, stored at
+            // row * 128 + ((piece ^ (row & 7)) << 4) (the 128-byte swizzle)
+            const int g = (int)threadIdx.x - 768;
+            const int piece = g & 7, r0 = g >> 3;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (long long u = t0; ok && u < tiles; u += dt) {
+                const PTile t = list.at(u);
+                int row[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int p = t.m0 + (int)rank * 128 + r0 + 16 * i;
+                    row[i] = p < t.m_end ? __ldg(a.gather + p) : -2;
+                    if (row[i] >= a.rows || row[i] == -1) row[i] = -1;
+                }
+                for (int kb = 0; kb < nk; ++kb) {
+                    bool w = true;
+                    if (lane == 0) w = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort);
+                    w = __shfl_sync(0xffffffffu, w, 0);
+                    if (!w) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sx = base + stage * kPStage;
+                    const int k0 = kb * kPK + piece * 16;
+                    const bool in = k0 < a.K;  // K is a multiple of 16
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = r0 + 16 * i;
+                        // rows past the segment's end feed only accumulator rows that are never
+                        // stored; a row outside `a` and the K past the end are zeros
+                        const bool rd = in && row[i] >= 0;
+                        if (row[i] != -2)
+                            cp_async_16_zfill(sx + rr * 128 + ((piece ^ (rr & 7)) << 4),
+                                              rd ? a.a + (size_t)row[i] * a.K + k0 : a.a, rd ? 16u : 0u);
+                    }
+                    cp_async_arrive_noinc(gfull_bar(stage));
+                    if (++stage == kPStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            cp_async_wait_all();
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (*abort) {
+        if (threadIdx.x == 0 && a.err) atomicOr(a.err, MOE_DEVERR_TIMEOUT);
+        const uint64_t w0 = globaltimer_ns();  // let copies and remote arrives already issued land
+        while (globaltimer_ns() - w0 < 2000000ull) {
+        }
+    }
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kPTmem);
+    }
+}
+
+template <int kMode, bool kGather>
+cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
+    auto *kernel = fp8_mx_pair_kernel<kMode, kGather>;
+    int unused = 0;
+    cudaError_t err = launch_setup_once((const void *)kernel, &unused, [&](int, int *v) -> cudaError_t {
+        *v = 1;
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)XCfg<kMode>::kSmem);
+    });
+    if (err != cudaSuccess) return err;
+    {
+        const uint64_t dims[3] = {(uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E};
+        const uint64_t strides[2] = {(uint64_t)a.K, (uint64_t)a.K * a.N};
+        const uint32_t box[3] = {kPK, 128, 1};
+        if (!make_map_u8(&a.tmap_w, a.w, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    if (!kGather) {
+        const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)a.rows};
+        const uint64_t strides[1] = {(uint64_t)a.K};
+        const uint32_t box[2] = {kPK, 128};
+        if (!make_map_u8(&a.tmap_a, a.a, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    if (kMode != kFp8SwiGlu && !make_map_16(&a.tmap_out, a.out, (uint64_t)a.N, (uint64_t)a.P, 64, 32))
+        return cudaErrorInvalidValue;
+    const int n_tiles = (a.N + kPN - 1) / kPN;
+    // no more row tiles than P / 256 and one begun per expert
+    const int64_t tiles = (a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
+    const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+    kernel<<<2 * clusters, x_threads(kGather), XCfg<kMode>::kSmem, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_mx_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
+    if (mode == kFp8SwiGlu) return launch_one<kFp8SwiGlu, true>(a, num_sms, s);
+    if (mode == kFp8Y16) return launch_one<kFp8Y16, false>(a, num_sms, s);
+    return a.gather ? launch_one<kFp8Bf16, true>(a, num_sms, s) : launch_one<kFp8Bf16, false>(a, num_sms, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,217 @@
+// What the two CTA-pair kernels of the block-scaled products share: the tile, the
+// per-expert table of row tiles, and the epilogue from a thread's 64 finished
+// accumulator columns to global memory.
+//
+// Tile: 256 rows of one segment x 256 weight rows, on a cluster of two CTAs.  CTA
+// r holds rows [128 r, 128 r + 128) of `a` and weight rows [128 r, 128 r + 128) of
+// each stage of 128 K (16 KB + 16 KB); the even CTA issues the pair MMA (M = 256,
+// N = 256, K = 32) for both, so each SM reads half the operand bytes per product
+// that a tile of its own would need.  With SwiGLU the 256 weight rows are 128
+// gates and their 128 ups.  Sixteen epilogue warps: four per TMEM lane quarter,
+// 64 columns each.
+#pragma once
+
+#include "fp8.cuh"
+
+namespace moe {
+
+#if defined(__CUDACC__)
+
+constexpr int kPM = 256;                    // rows per tile
+constexpr int kPN = 256;                    // weight rows per tile
+constexpr int kPK = 128;                    // K per stage = one scale block
+constexpr uint32_t kPHalf = 128 * kPK;      // 16 KB: one CTA's share of an operand stage
+constexpr uint32_t kPStage = 2 * kPHalf;
+constexpr int kPGather = 128;               // gather threads
+constexpr int kPEpiWarps = 16;
+constexpr uint32_t kPTmem = 512;
+constexpr uint32_t kPStore = 32 * 128;      // per epilogue warp: 32 rows x 64 16-bit columns
+
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+__device__ __forceinline__ void p_epilogue_bar() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+
+struct PTile {
+    int e, nt, m0, m_end;
+};
+
+// The tile list: row tiles expert by expert, each row tile's weight tiles together
+// (neighbouring clusters share its rows in L2).  off_s and pre_s are shared-memory
+// tables of E + 1 entries.
+struct PTiles {
+    const int *off_s, *pre_s;
+    int E, N, n_tiles;
+    bool concat;
+    __device__ __forceinline__ long long count() const { return (long long)pre_s[E] * n_tiles; }
+    __device__ __forceinline__ PTile at(long long u) const {
+        PTile t;
+        const int mt = (int)(u / n_tiles);
+        t.nt = (int)(u - (long long)mt * n_tiles);
+        int lo = 0, hi = E - 1;  // largest e with pre_s[e] <= mt
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre_s[mid] <= mt) lo = mid;
+            else hi = mid - 1;
+        }
+        t.e = lo;
+        t.m0 = off_s[lo] + (mt - pre_s[lo]) * kPM;
+        t.m_end = off_s[lo + 1];
+        return t;
+    }
+    // first weight row of half h (accumulator columns 128 h ..) of a tile
+    __device__ __forceinline__ int wrow(int nt, int h) const {
+        return concat ? h * (N / 2) + nt * 128 : nt * kPN + h * 128;
+    }
+};
+
+// Segment offsets into off_s, held inside [0, P] whatever the caller's table says.
+__device__ __forceinline__ void load_offsets(const Fp8GemmArgs &a, int *off_s, int threads) {
+    if (a.expert_off) {
+        for (int i = threadIdx.x; i <= a.E; i += threads)
+            off_s[i] = (int)min(max((long long)__ldcg(a.expert_off + i), 0ll), (long long)a.P);
+    } else if (threadIdx.x < 2) {
+        off_s[threadIdx.x] = threadIdx.x ? (int)a.P : 0;
+    }
+}
+// pre_s[e] = pieces of `rows` rows in the experts below e (one converged warp).
+__device__ __forceinline__ void prefix_pieces(const int *off_s, int *pre_s, int E, int rows, int lane) {
+    int sum = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = e < E ? (max(off_s[e + 1] - off_s[e], 0) + rows - 1) / rows : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (e < E) pre_s[e] = sum + incl - n;
+        sum += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) pre_s[E] = sum;
+}
+
+// 64 16-bit columns (32 packed pairs) of one row per lane: a warp whose 32 rows
+// are all stored goes through shared memory and one TMA store (columns past N
+// are clipped); otherwise each valid lane stores its row.
+__device__ __forceinline__ void store64(const CUtensorMap *map, uint32_t buf, int lane, bool warp_full, bool valid,
+                                        int row0, uint16_t *row, int col0, int N, const uint32_t (&v)[32]) {
+    if (warp_full) {
+        if (lane == 0) bulk_wait_read0();  // the buffer's previous store has been read
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            st_shared_v4(buf + lane * 128 + ((c ^ (lane & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2],
+                         v[4 * c + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, buf, col0, row0);
+            bulk_commit();
+        }
+    } else if (valid) {
+        uint4 *dst = reinterpret_cast<uint4 *>(row + col0);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (col0 + 8 * c < N) dst[c] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    }
+}
+
+// One epilogue thread's part of a finished tile: row r of this CTA's 128 and 64
+// accumulator columns acc -- the tile's columns [64 cq, 64 cq + 64), or, with
+// concatenated SwiGLU, gates [32 cq, 32 cq + 32) and their ups.  buf: the warp's
+// store buffer; max_s: [4][128] row maxima (SwiGLU).  All 16 warps call it.
+template <int kMode>
+__device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t, float (&acc)[64], int rank, int cq,
+                                            int q4, int lane, bool concat, uint32_t buf, float *max_s, bool ok) {
+    const int r = 32 * q4 + lane;
+    const int row0 = t.m0 + rank * 128 + q4 * 32;
+    const int p = row0 + lane;
+    const bool store = ok && p < t.m_end;
+    if (kMode != kFp8SwiGlu) {
+        const int col = t.nt * kPN + cq * 64;
+        if (col < a.N) {
+            if (a.bias) {
+                const __nv_bfloat16 *br = a.bias + (size_t)t.e * a.N + col;
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    if (col + j < a.N) acc[j] += __bfloat162float(br[j]);
+            }
+            if (kMode == kFp8Y16) {  // fp16 scaled by a power of two per 32 columns
+                uint32_t exps = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float m = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) m = amax_of(m, acc[32 * i + j]);
+                    const int ex = y_block_exp(m);
+                    const float sc = exp2i(-ex);
+                    exps |= (uint32_t)(uint8_t)(int8_t)ex << (8 * i);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[32 * i + j] *= sc;
+                }
+                if (store)  // N is a multiple of 128: the two exponents are one aligned half-word
+                    *reinterpret_cast<uint16_t *>(static_cast<int8_t *>(a.out_scale) +
+                                                  (size_t)p * (a.N / kYBlock) + col / kYBlock) = (uint16_t)exps;
+            }
+            uint32_t v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = kMode == kFp8Y16 ? pack_f16x2(acc[2 * j], acc[2 * j + 1])
+                                        : pack_bf16x2(acc[2 * j], acc[2 * j + 1]);
+            store64(&a.tmap_out, buf, lane, ok && row0 + 31 < t.m_end, store, row0,
+                    static_cast<uint16_t *>(a.out) + (size_t)(store ? p : 0) * a.N, col, a.N, v);
+        }
+    } else {
+        // h = silu(gate) up: 32 columns per thread, with the other three quarters' one scale block
+        const int hc = t.nt * 128 + cq * 32;  // first h column of this thread
+        if (a.bias) {
+            const __nv_bfloat16 *br = a.bias + (size_t)t.e * a.N;
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+                const int col = concat ? (j < 32 ? hc + j : a.N / 2 + hc + j - 32) : 2 * hc + j;
+                acc[j] += __bfloat162float(br[col]);
+            }
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            // interleaved: columns 2j, 2j+1; the value goes to acc[j], whose own column
+            // has been used by then (j <= 2j)
+            const float g = concat ? acc[j] : acc[2 * j], up = concat ? acc[32 + j] : acc[2 * j + 1];
+            const float h = inf_to_nan(__fdividef(g, 1.0f + __expf(-g)) * up);
+            acc[j] = h;
+            m = amax_of(m, h);
+        }
+        max_s[cq * 128 + r] = m;
+        p_epilogue_bar();
+        m = fmaxf(fmaxf(max_s[r], max_s[128 + r]), fmaxf(max_s[256 + r], max_s[384 + r]));
+        const uint32_t e = e4m3_scale_exp(m);
+        const float is = inv_scale_of_exp(e);
+        if (store) {
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + (size_t)p * (a.N / 2) + hc);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = 16 * i + 4 * k;
+                    v[k] = pack_e4m3x4(acc[j] * is, acc[j + 1] * is, acc[j + 2] * is, acc[j + 3] * is);
+                }
+                o[i] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+            if (cq == 0) static_cast<uint8_t *>(a.out_scale)[(size_t)p * (a.N / 256) + t.nt] = (uint8_t)e;
+        }
+        p_epilogue_bar();  // max_s has been read
+    }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace moe
