@@ -21,7 +21,7 @@ struct Fp8GemmArgs {
     const uint8_t *w;           // weights [E, N, K] e4m3
     CUtensorMap tmap_w;         // `w` as (K, N rows, E), box 128 x 128 x 1 (made by the launch)
     CUtensorMap tmap_a;         // `a` as (K, rows), box 128 x one chunk (made by the launch; unused when gathered)
-    CUtensorMap tmap_out;       // pair kernel: `out` as [P][N] 16-bit, box 64 columns x 32 rows (made by the launch)
+    CUtensorMap tmap_out;       // pair kernel: `out` as [P][N] 16-bit, box 32 columns x 32 rows (made by the launch)
     const uint8_t *a;           // rows [rows, K] e4m3
     const void *a_scale;        // [rows, nk]
     const void *w_scale;        // [E, ceil(N/128), nk]
@@ -77,8 +77,8 @@ int current_device_sms(int *sms);  // MOE_OK and the SM count, or the status to 
 // e4m3 tensor map: dims/strides/box innermost first, 128-byte swizzle, zero fill.
 bool make_map_u8(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
                  const uint32_t *box);
-// 16-bit [rows][cols] tensor map for stores.
-bool make_map_16(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows);
+// 16-bit [rows][cols] tensor map for stores of 32 x 32 boxes, 64-byte swizzle.
+bool make_map_out16(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows);
 
 #if defined(__CUDACC__)
 

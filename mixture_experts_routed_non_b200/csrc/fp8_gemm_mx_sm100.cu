@@ -40,9 +40,9 @@ constexpr uint32_t kXScaleCols = 16;  // TMEM columns of a stage's scales: `a` a
 
 template <int kMode>
 struct XCfg {
-    // 16-bit outputs pass through 64 KB of store buffers; the e4m3 rows of SwiGLU are whole
+    // 16-bit outputs pass through 32 KB of store buffers; the e4m3 rows of SwiGLU are whole
     // sectors per thread and are stored directly
-    static constexpr int kStages = kMode == kFp8SwiGlu ? 6 : 4;
+    static constexpr int kStages = kMode == kFp8SwiGlu ? 6 : 5;
     static constexpr int kBars = 3 * kStages + 3;
     static constexpr size_t kStoreOff = (size_t)kStages * kPStage;
     static constexpr size_t kMaxOff = kStoreOff + (kMode == kFp8SwiGlu ? 0 : kPEpiWarps * kPStore);  // [4][128]
@@ -322,59 +322,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
                 acc[j] = __uint_as_float(v0[j]);
                 acc[32 + j] = __uint_as_float(v1[j]);
             }
-            pair_output<kMode>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s, *abort == 0);
+            pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s, *abort == 0);
         }
         if (lane == 0) bulk_wait0();  // this warp's stores are complete
     } else {
         regs_dec<x_other_regs(kGather)>();
-        if (kGather) {
-            // --------------------------------------------------- row gather
-            // thread g: 16-byte piece (g & 7) of rows (g >> 3) + 16 i, stored at
-            // row * 128 + ((piece ^ (row & 7)) << 4) (the 128-byte swizzle)
-            const int g = (int)threadIdx.x - 768;
-            const int piece = g & 7, r0 = g >> 3;
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (long long u = t0; ok && u < tiles; u += dt) {
-                const PTile t = list.at(u);
-                int row[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int p = t.m0 + (int)rank * 128 + r0 + 16 * i;
-                    row[i] = p < t.m_end ? __ldg(a.gather + p) : -2;
-                    if (row[i] >= a.rows || row[i] == -1) row[i] = -1;
-                }
-                for (int kb = 0; kb < nk; ++kb) {
-                    bool w = true;
-                    if (lane == 0) w = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort);
-                    w = __shfl_sync(0xffffffffu, w, 0);
-                    if (!w) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sx = base + stage * kPStage;
-                    const int k0 = kb * kPK + piece * 16;
-                    const bool in = k0 < a.K;  // K is a multiple of 16
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = r0 + 16 * i;
-                        // rows past the segment's end feed only accumulator rows that are never
-                        // stored; a row outside `a` and the K past the end are zeros
-                        const bool rd = in && row[i] >= 0;
-                        if (row[i] != -2)
-                            cp_async_16_zfill(sx + rr * 128 + ((piece ^ (rr & 7)) << 4),
-                                              rd ? a.a + (size_t)row[i] * a.K + k0 : a.a, rd ? 16u : 0u);
-                    }
-                    cp_async_arrive_noinc(gfull_bar(stage));
-                    if (++stage == kPStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-            cp_async_wait_all();
-        }
+        if (kGather)
+            gather_rows<kPStages>(a, list, (int)rank, (int)threadIdx.x - 768, base, empty_bar, gfull_bar, abort, t0, dt);
     }
 
     // ---------------------------------------------------------------- teardown
@@ -414,7 +368,7 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
         const uint32_t box[2] = {kPK, 128};
         if (!make_map_u8(&a.tmap_a, a.a, 2, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    if (kMode != kFp8SwiGlu && !make_map_16(&a.tmap_out, a.out, (uint64_t)a.N, (uint64_t)a.P, 64, 32))
+    if (kMode != kFp8SwiGlu && !make_map_out16(&a.tmap_out, a.out, (uint64_t)a.N, (uint64_t)a.P))
         return cudaErrorInvalidValue;
     const int n_tiles = (a.N + kPN - 1) / kPN;
     // no more row tiles than P / 256 and one begun per expert

@@ -22,10 +22,10 @@ constexpr int kPN = 256;                    // weight rows per tile
 constexpr int kPK = 128;                    // K per stage = one scale block
 constexpr uint32_t kPHalf = 128 * kPK;      // 16 KB: one CTA's share of an operand stage
 constexpr uint32_t kPStage = 2 * kPHalf;
-constexpr int kPGather = 128;               // gather threads
+constexpr int kPGather = 128;               // gather threads of a CTA
 constexpr int kPEpiWarps = 16;
 constexpr uint32_t kPTmem = 512;
-constexpr uint32_t kPStore = 32 * 128;      // per epilogue warp: 32 rows x 64 16-bit columns
+constexpr uint32_t kPStore = 32 * 64;       // per epilogue warp: 32 rows x 32 16-bit columns
 
 template <int R>
 __device__ __forceinline__ void regs_inc() {
@@ -97,17 +97,17 @@ __device__ __forceinline__ void prefix_pieces(const int *off_s, int *pre_s, int 
     if (lane == 0) pre_s[E] = sum;
 }
 
-// 64 16-bit columns (32 packed pairs) of one row per lane: a warp whose 32 rows
-// are all stored goes through shared memory and one TMA store (columns past N
-// are clipped); otherwise each valid lane stores its row.
-__device__ __forceinline__ void store64(const CUtensorMap *map, uint32_t buf, int lane, bool warp_full, bool valid,
-                                        int row0, uint16_t *row, int col0, int N, const uint32_t (&v)[32]) {
+// 32 16-bit columns (16 packed pairs) of one row per lane: a warp whose 32 rows
+// are all stored goes through shared memory (64-byte swizzle) and one TMA store
+// (columns past N are clipped); otherwise each valid lane stores its row.
+__device__ __forceinline__ void store32(const CUtensorMap *map, uint32_t buf, int lane, bool warp_full, bool valid,
+                                        int row0, uint16_t *row, int col0, int N, const uint32_t (&v)[16]) {
     if (warp_full) {
         if (lane == 0) bulk_wait_read0();  // the buffer's previous store has been read
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            st_shared_v4(buf + lane * 128 + ((c ^ (lane & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2],
+        for (int c = 0; c < 4; ++c)
+            st_shared_v4(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2],
                          v[4 * c + 3]);
         fence_proxy_async_smem();
         __syncwarp();
@@ -118,22 +118,74 @@ __device__ __forceinline__ void store64(const CUtensorMap *map, uint32_t buf, in
     } else if (valid) {
         uint4 *dst = reinterpret_cast<uint4 *>(row + col0);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < 4; ++c)
             if (col0 + 8 * c < N) dst[c] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
     }
+}
+
+// The row gather of one CTA's stages, by 128 threads: thread g copies the 16-byte
+// piece (g & 7) of rows (g >> 3) + 16 i to row * 128 + ((piece ^ (row & 7)) << 4)
+// (the 128-byte swizzle).  Rows past the segment's end feed only accumulator rows
+// that are never stored and are not copied.  Every copy reads a valid address
+// unconditionally -- a row outside `a` some other row (pair_output drops what it
+// gave), a piece past the end of K the row's last one (the weights are zeros
+// there) -- because a choice between two sources, or the copy's own zero fill,
+// cost a third to two thirds of the whole product (131072 x 2048 x 1536 over 128
+// experts: 358 us like this, 465 with a zero row, 547 with zero fill).
+template <int kStages, typename Empty, typename Gfull>
+__device__ __forceinline__ void gather_rows(const Fp8GemmArgs &a, const PTiles &list, int rank, int g, uint32_t base,
+                                            Empty empty_bar, Gfull gfull_bar, volatile uint32_t *abort, long long t0,
+                                            long long dt) {
+    const int piece = g & 7, r0 = g >> 3;
+    const long long tiles = list.count();
+    int stage = 0;
+    uint32_t phase = 0;
+    for (long long u = t0; u < tiles; u += dt) {
+        const PTile t = list.at(u);
+        int row[8];  // -1: not copied
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int p = t.m0 + rank * 128 + r0 + 16 * i;
+            row[i] = p < t.m_end ? (int)min((long long)max(__ldg(a.gather + p), 0), (long long)a.rows - 1) : -1;
+        }
+        for (int kb = 0; kb < a.nk; ++kb) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort))) {
+                cp_async_wait_all();
+                return;
+            }
+            const uint32_t dst = base + stage * kPStage + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
+            const uint8_t *src = a.a + min(kb * kPK + piece * 16, a.K - 16);  // K is a multiple of 16
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (row[i] >= 0) cp_async_16(dst + i * 2048, src + (size_t)row[i] * a.K);
+            cp_async_arrive_noinc(gfull_bar(stage));
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    cp_async_wait_all();
 }
 
 // One epilogue thread's part of a finished tile: row r of this CTA's 128 and 64
 // accumulator columns acc -- the tile's columns [64 cq, 64 cq + 64), or, with
 // concatenated SwiGLU, gates [32 cq, 32 cq + 32) and their ups.  buf: the warp's
 // store buffer; max_s: [4][128] row maxima (SwiGLU).  All 16 warps call it.
-template <int kMode>
+template <int kMode, bool kGather>
 __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t, float (&acc)[64], int rank, int cq,
                                             int q4, int lane, bool concat, uint32_t buf, float *max_s, bool ok) {
     const int r = 32 * q4 + lane;
     const int row0 = t.m0 + rank * 128 + q4 * 32;
     const int p = row0 + lane;
     const bool store = ok && p < t.m_end;
+    if (kGather && p < t.m_end) {  // a gathered row outside `a` counts as zeros
+        const int src = __ldg(a.gather + p);
+        if (src < 0 || src >= a.rows) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0.f;
+        }
+    }
     if (kMode != kFp8SwiGlu) {
         const int col = t.nt * kPN + cq * 64;
         if (col < a.N) {
@@ -160,13 +212,17 @@ __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t
                     *reinterpret_cast<uint16_t *>(static_cast<int8_t *>(a.out_scale) +
                                                   (size_t)p * (a.N / kYBlock) + col / kYBlock) = (uint16_t)exps;
             }
-            uint32_t v[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                v[j] = kMode == kFp8Y16 ? pack_f16x2(acc[2 * j], acc[2 * j + 1])
-                                        : pack_bf16x2(acc[2 * j], acc[2 * j + 1]);
-            store64(&a.tmap_out, buf, lane, ok && row0 + 31 < t.m_end, store, row0,
-                    static_cast<uint16_t *>(a.out) + (size_t)(store ? p : 0) * a.N, col, a.N, v);
+            for (int i = 0; i < 2; ++i) {
+                uint32_t v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] = kMode == kFp8Y16 ? pack_f16x2(acc[32 * i + 2 * j], acc[32 * i + 2 * j + 1])
+                                            : pack_bf16x2(acc[32 * i + 2 * j], acc[32 * i + 2 * j + 1]);
+                if (col + 32 * i < a.N)
+                    store32(&a.tmap_out, buf, lane, ok && row0 + 31 < t.m_end, store, row0,
+                            static_cast<uint16_t *>(a.out) + (size_t)(store ? p : 0) * a.N, col + 32 * i, a.N, v);
+            }
         }
     } else {
         // h = silu(gate) up: 32 columns per thread, with the other three quarters' one scale block
