@@ -19,11 +19,11 @@
 // whole accumulator into registers (64 per thread) and hands it back; conversion
 // and stores run behind the next tile's MMAs.
 //
-// Warp roles: 0 = TMA producer, 1 = TMEM allocator and MMA issuer (even CTA), 2 =
-// gather relay (fp8_gemm_pair_sm100.cu), 4-7 = scales, 8-23 = epilogue, 24-27 =
+// Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer (even
+// CTA), 2 = TMA of the rows or gather relay (fp8_gemm_pair_sm100.cu), 4-7 = scales, 8-23 = epilogue, 24-27 =
 // row gather (gathered rows only).  Registers are moved to the epilogue warps
-// (setmaxnreg: with gathered rows 4 x 96 + 3 x 40 per thread of the seven
-// warpgroups, the 7 x 72 of the launch; else 4 x 96 + 2 x 48 = 6 x 80).  Every wait
+// (setmaxnreg: with gathered rows 4 x 88 + 3 x 48 per thread of the seven
+// warpgroups, within the 7 x 72 of the launch; else 4 x 96 + 2 x 48 = 6 x 80).  Every wait
 // is bounded (common.cuh).
 #include "fp8_pair.cuh"
 
@@ -32,10 +32,10 @@ namespace {
 
 // registers per thread of the launch, of the epilogue warpgroups and of the others
 __host__ __device__ constexpr int x_threads(bool gather) { return gather ? 896 : 768; }
-__host__ __device__ constexpr int x_other_regs(bool gather) { return gather ? 40 : 48; }
-constexpr int kXEpiRegs = 96;
-static_assert(4 * kXEpiRegs + 3 * x_other_regs(true) == 7 * 72 && 4 * kXEpiRegs + 2 * x_other_regs(false) == 6 * 80,
-              "the warpgroups' registers are those of the launch");
+__host__ __device__ constexpr int x_epi_regs(bool gather) { return gather ? 88 : 96; }
+constexpr int kXOtherRegs = 48;
+static_assert(4 * x_epi_regs(true) + 3 * kXOtherRegs <= 7 * 72 && 4 * x_epi_regs(false) + 2 * kXOtherRegs <= 6 * 80,
+              "the warpgroups' registers are no more than those of the launch");
 constexpr uint32_t kXScaleCols = 16;  // TMEM columns of a stage's scales: `a` at 0, weights at 8
 
 template <int kMode>
@@ -78,12 +78,26 @@ __device__ __forceinline__ void tmem_st_x4(uint32_t taddr, uint32_t r0, uint32_t
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The e8m0 bytes of blocks kb .. kb + 3 (the last block repeated behind the end) in one word.
-__device__ __forceinline__ uint32_t load_e8m0_x4(const uint8_t *p, size_t i, int last) {
+// The e8m0 bytes i .. i + 3 of a row of scales, as two registers that make up one
+// word by r0 | r1 << 16 -- later: nothing here waits for the loads, except where a
+// row starts at an odd byte.  how: 0 rows of whole words, 1 of half-words, 2 bytes.
+__device__ __forceinline__ void load_e8m0_x4(const uint8_t *p, size_t i, int last, int how, uint32_t &r0, uint32_t &r1) {
     const uint8_t *q = p + i;
-    if (last >= 3 && (reinterpret_cast<uintptr_t>(q) & 3) == 0) return __ldg(reinterpret_cast<const uint32_t *>(q));
-    const uint32_t b0 = __ldg(q), b1 = __ldg(q + min(1, last)), b2 = __ldg(q + min(2, last)), b3 = __ldg(q + min(3, last));
-    return b0 | b1 << 8 | b2 << 16 | b3 << 24;
+    r1 = 0;
+    if (how == 0) {
+        r0 = __ldg(reinterpret_cast<const uint32_t *>(q));
+    } else if (how == 1) {
+        r0 = __ldg(reinterpret_cast<const uint16_t *>(q));
+        if (last >= 2) r1 = __ldg(reinterpret_cast<const uint16_t *>(q + 2));
+    } else {  // behind `last` the last byte again: never used
+        const uint32_t b0 = __ldg(q), b1 = __ldg(q + min(1, last)), b2 = __ldg(q + min(2, last)),
+                       b3 = __ldg(q + min(3, last));
+        r0 = b0 | b1 << 8 | b2 << 16 | b3 << 24;
+    }
+}
+__device__ __forceinline__ int e8m0_rows(const uint8_t *p, int nk) {
+    const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(p) | (uint32_t)nk;
+    return (a & 3) == 0 ? 0 : (a & 1) == 0 ? 1 : 2;
 }
 
 template <int kMode, bool kGather>
@@ -146,28 +160,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     const int nk = a.nk;
     const bool concat = kMode == kFp8SwiGlu && a.layout == MOE_LAYOUT_CONCATENATED;
     const PTiles list{off_s, pre_s, E, a.N, (a.N + kPN - 1) / kPN, concat};
-    const long long tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
+    const int tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
 
     if (warp < 4) {
-        regs_dec<x_other_regs(kGather)>();
-        if (warp == 0 && lane == 0) {
-            // -------------------------------------------------------- producer
+        regs_dec<kXOtherRegs>();
+        if (warp == 0) {
+            // ------------------------------------------------ producer: weights
+            const bool leader = elect_one();
+            const uint32_t full0 = mapa_shared(full_bar(0), 0);
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_parity = 0;
             bool ok = true;
-            for (long long u = t0; ok && u < tiles; u += dt) {
+            for (int u = t0; ok && u < tiles; u += dt) {
                 const PTile t = list.at(u);
-                const int wr = list.wrow(t.nt, (int)rank), ar = t.m0 + 128 * (int)rank;
+                const int wr = list.wrow(t.nt, (int)rank);
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort)) {
-                        ok = false;
-                        break;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
+                    if (!ok) break;
+                    if (leader) {
+                        // both CTAs' TMA bytes (weights, and rows that are not gathered) land on
+                        // the even CTA's barrier
+                        if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), kGather ? 2 * kPHalf : 4 * kPHalf);
+                        tma_load_3d_pair(base + stage * kPStage + kPHalf, &a.tmap_w, full0 + 8u * stage, kb * kPK, wr,
+                                         t.e);
                     }
-                    // both CTAs' TMA bytes land on the even CTA's barrier
-                    if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), kGather ? 2 * kPHalf : 4 * kPHalf);
-                    const uint32_t fb = mapa_shared(full_bar(stage), 0), dst = base + stage * kPStage;
-                    tma_load_3d_pair(dst + kPHalf, &a.tmap_w, fb, kb * kPK, wr, t.e);
-                    if (!kGather) tma_load_2d_pair(dst, &a.tmap_a, fb, kb * kPK, ar);
+                    __syncwarp();
                     issued |= 1u << stage;
                     issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
                     if (++stage == kPStages) {
@@ -178,9 +195,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             }
             // the even CTA's full barriers count both CTAs' bytes: wait for every phase this
             // CTA issued before the CTA may exit
-            if (rank == 0)
+            if (rank == 0 && leader)
                 for (int s = 0; s < kPStages; ++s)
                     if ((issued & (1u << s)) && !mbar_wait_timed(full_bar(s), (issued_parity >> s) & 1u)) *abort = 1u;
+        } else if (!kGather && warp == 2) {
+            // --------------------------------------------------- producer: rows
+            const bool leader = elect_one();
+            const uint32_t full0 = mapa_shared(full_bar(0), 0);
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = t0; ok && u < tiles; u += dt) {
+                const PTile t = list.at(u);
+                const int ar = t.m0 + 128 * (int)rank;
+                for (int kb = 0; kb < nk; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
+                    if (!ok) break;
+                    if (leader)
+                        tma_load_2d_pair(base + stage * kPStage, &a.tmap_a, full0 + 8u * stage, kb * kPK, ar);
+                    __syncwarp();
+                    if (++stage == kPStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
         } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------------ MMA issuer
             int stage = 0;
@@ -191,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             // steps only move the start address (16-byte units, below 2^14), so the issue loop adds
             const uint64_t desc0 = smem_desc_sw128(base, 16, 1024);
             const bool leader = elect_one();
-            for (long long u = t0; ok && u < tiles; u += dt, tphase ^= 1u) {
+            for (int u = t0; ok && u < tiles; u += dt, tphase ^= 1u) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(tempty_bar, tphase ^ 1u, abort));
                 for (int kb = 0; ok && kb < nk; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort));
@@ -223,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (long long u = t0; ok && u < tiles; u += dt)
+            for (int u = t0; ok && u < tiles; u += dt)
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait_bounded(gfull_bar(stage), phase, abort)) {
                         ok = false;
@@ -239,51 +278,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         }
         __syncwarp();
     } else if (warp < 8) {
-        regs_dec<x_other_regs(kGather)>();
+        regs_dec<kXOtherRegs>();
         // ------------------------------------------------------------ scales
         const int nb = (a.N + 127) / 128;
         const uint8_t *as = static_cast<const uint8_t *>(a.a_scale), *ws = static_cast<const uint8_t *>(a.w_scale);
         const uint32_t sf0 = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + kPN;
+        const uint32_t full0 = mapa_shared(full_bar(0), 0);
         int stage = 0;
         uint32_t phase = 0;
-        bool ok = true;
-        for (long long u = t0; ok && u < tiles; u += dt) {
-            const PTile t = list.at(u);
-            int srow[4];  // rows of `a`; -1: past the segment or outside `a` (their codes are zeros or never used)
+        // The words of the next four blocks are loaded before the current four are handed over,
+        // and a tile's row numbers a tile ahead: a tile's first scales would otherwise be two
+        // dependent loads (thousands of clocks under load) behind the operands.
+        PTile t;
+        int srow[4], nrow[4];  // rows of `a`; -1: past the segment or outside `a` (zeros, or never stored)
+        size_t wi[2];
+        uint32_t ra[4][2], rw[2][2];
+        const int ha = e8m0_rows(as, nk), hw = e8m0_rows(ws, nk);
+        auto load_rows = [&](int u) {
+            if (u < tiles) t = list.at(u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int p = t.m0 + (int)rank * 128 + 32 * i + lane;
-                srow[i] = p < t.m_end ? (kGather ? __ldg(a.gather + p) : p) : -1;
-                if (srow[i] >= a.rows) srow[i] = -1;
+                nrow[i] = u < tiles && p < t.m_end ? (kGather ? __ldg(a.gather + p) : p) : -1;
             }
-            size_t wi[2];  // (a half past the end of N has no scales: its columns are never stored)
+        };
+        auto enter_tile = [&]() {  // the tile load_rows has just been called for
+#pragma unroll
+            for (int i = 0; i < 4; ++i) srow[i] = nrow[i] < a.rows ? nrow[i] : -1;
+            // (a half past the end of N has no scales: its columns are never stored)
 #pragma unroll
             for (int h = 0; h < 2; ++h) wi[h] = ((size_t)t.e * nb + min(list.wrow(t.nt, h) / 128, nb - 1)) * nk;
+        };
+        auto load_group = [&](int kb) {
+            const int last = nk - 1 - kb;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ra[i][0] = 0x7F7F7F7Fu;
+                ra[i][1] = 0;
+                if (srow[i] >= 0) load_e8m0_x4(as, (size_t)srow[i] * nk + kb, last, ha, ra[i][0], ra[i][1]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) load_e8m0_x4(ws, wi[h] + kb, last, hw, rw[h][0], rw[h][1]);
+        };
+        bool ok = true;
+        if (t0 < tiles) {
+            load_rows(t0);
+            enter_tile();
+            load_group(0);
+            load_rows(t0 + dt);
+        }
+        for (int u = t0; ok && u < tiles; u += dt) {
             for (int kb = 0; ok && kb < nk; kb += 4) {
-                uint32_t ra[4], rw[2];
-                const int last = nk - 1 - kb;
+                uint32_t ca[4], cw[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    ra[i] = srow[i] >= 0 ? load_e8m0_x4(as, (size_t)srow[i] * nk + kb, last) : 0x7F7F7F7Fu;
+                for (int i = 0; i < 4; ++i) ca[i] = ra[i][0] | ra[i][1] << 16;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) rw[h] = load_e8m0_x4(ws, wi[h] + kb, last);
+                for (int h = 0; h < 2; ++h) cw[h] = rw[h][0] | rw[h][1] << 16;
+                if (kb + 4 < nk) {
+                    load_group(kb + 4);
+                } else if (u + dt < tiles) {
+                    enter_tile();
+                    load_group(0);
+                    load_rows(u + 2 * dt);
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (k > last) break;
+                    if (kb + k >= nk) break;
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                     if (!ok) break;
                     const uint32_t sel = 0x1111u * (uint32_t)k;  // byte k four times
                     const uint32_t sf = sf0 + (uint32_t)stage * kXScaleCols;
-                    const uint32_t w0 = __byte_perm(rw[0], 0, sel), w1 = __byte_perm(rw[1], 0, sel);
+                    const uint32_t w0 = __byte_perm(cw[0], 0, sel), w1 = __byte_perm(cw[1], 0, sel);
                     tc_fence_after();
-                    tmem_st_x4(sf, __byte_perm(ra[0], 0, sel), __byte_perm(ra[1], 0, sel), __byte_perm(ra[2], 0, sel),
-                               __byte_perm(ra[3], 0, sel));
+                    tmem_st_x4(sf, __byte_perm(ca[0], 0, sel), __byte_perm(ca[1], 0, sel), __byte_perm(ca[2], 0, sel),
+                               __byte_perm(ca[3], 0, sel));
                     tmem_st_x4(sf + 8, w0, w0, w0, w0);
                     tmem_st_x4(sf + 12, w1, w1, w1, w1);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(full_bar(stage), 0));
+                    if (lane == 0) mbar_arrive_cluster(full0 + 8u * stage);
                     if (++stage == kPStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -292,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             }
         }
     } else if (warp < 24) {
-        regs_inc<kXEpiRegs>();
+        regs_inc<x_epi_regs(kGather)>();
         // ------------------------------------------------------------ epilogue
         const int q4 = warp & 3, cq = (warp - 8) >> 2;
         const uint32_t buf = base + (uint32_t)C::kStoreOff + (uint32_t)(warp - 8) * kPStore;
@@ -304,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         uint32_t tphase = 0;
         // a wait that gives up raises the abort flag; the warp then runs on over whatever is there
         // (later waits give up at once), meets the named barriers, and stores nothing
-        for (long long u = t0; u < tiles; u += dt, tphase ^= 1u) {
+        for (int u = t0; u < tiles; u += dt, tphase ^= 1u) {
             const PTile t = list.at(u);
             mbar_wait_bounded(tfull_bar, tphase, abort);
             __syncwarp();
@@ -326,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         }
         if (lane == 0) bulk_wait0();  // this warp's stores are complete
     } else {
-        regs_dec<x_other_regs(kGather)>();
+        regs_dec<kXOtherRegs>();
         if (kGather)
             gather_rows<kPStages>(a, list, (int)rank, (int)threadIdx.x - 768, base, empty_bar, gfull_bar, abort, t0, dt);
     }
@@ -373,6 +447,7 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     const int n_tiles = (a.N + kPN - 1) / kPN;
     // no more row tiles than P / 256 and one begun per expert
     const int64_t tiles = (a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;  // 32-bit tile numbers in the kernel
     const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
     kernel<<<2 * clusters, x_threads(kGather), XCfg<kMode>::kSmem, s>>>(a);
     return cudaGetLastError();

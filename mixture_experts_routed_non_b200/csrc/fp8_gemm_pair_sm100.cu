@@ -9,8 +9,8 @@
 // epilogue warp spends there is latency (barrier, TMEM load, arithmetic in
 // turn), which four warps per scheduler hide where two did not.
 //
-// Warp roles (24 warps): 0 = TMA producer, 1 = TMEM allocator and MMA issuer
-// (even CTA), 2 = gather relay, 3 = scale loader, 4-19 = epilogue, 20-23 = row
+// Warp roles (24 warps): 0 = TMA of the weights, 1 = TMEM allocator and MMA
+// issuer (even CTA), 2 = TMA of the rows or gather relay, 3 = scale loader, 4-19 = epilogue, 20-23 = row
 // gather (gathered rows only).  The scale loader runs up to eight blocks ahead
 // and leaves sa sw per row and weight half in shared memory, four blocks per
 // slot, so that no epilogue warp waits for global memory.  The relay turns the
@@ -18,7 +18,7 @@
 // fence that the tensor cores' reads of them need.  Registers are moved to the
 // epilogue warps (setmaxnreg: with gathered rows 4 x 104 + 2 x 32 per thread of
 // the six warpgroups, the 6 x 80 of the launch; else 4 x 112 + 32 = 5 x 96).
-// The MMA warp runs converged and elects the issuing lane only around the
+// The TMA and MMA warps run converged and elect the issuing lane only around the
 // instructions themselves, so that descriptors stay in uniform registers.
 // Every wait is bounded (common.cuh).
 #include "fp8_pair.cuh"
@@ -130,28 +130,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
     const int nk = a.nk;
     const bool concat = kMode == kFp8SwiGlu && a.layout == MOE_LAYOUT_CONCATENATED;
     const PTiles list{off_s, pre_s, E, a.N, (a.N + kPN - 1) / kPN, concat};
-    const long long tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
+    const int tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
 
     if (warp < 4) {
         regs_dec<kPOtherRegs>();
-        if (warp == 0 && lane == 0) {
-            // -------------------------------------------------------- producer
+        if (warp == 0) {
+            // ------------------------------------------------ producer: weights
+            const bool leader = elect_one();
+            const uint32_t full0 = mapa_shared(full_bar(0), 0);
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_parity = 0;
             bool ok = true;
-            for (long long u = t0; ok && u < tiles; u += dt) {
+            for (int u = t0; ok && u < tiles; u += dt) {
                 const PTile t = list.at(u);
-                const int wr = list.wrow(t.nt, (int)rank), ar = t.m0 + 128 * (int)rank;
+                const int wr = list.wrow(t.nt, (int)rank);
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort)) {
-                        ok = false;
-                        break;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
+                    if (!ok) break;
+                    if (leader) {
+                        // both CTAs' TMA bytes (weights, and rows that are not gathered) land on
+                        // the even CTA's barrier
+                        if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), kGather ? 2 * kPHalf : 4 * kPHalf);
+                        tma_load_3d_pair(base + stage * kPStage + kPHalf, &a.tmap_w, full0 + 8u * stage, kb * kPK, wr,
+                                         t.e);
                     }
-                    // both CTAs' TMA bytes land on the even CTA's barrier
-                    if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), kGather ? 2 * kPHalf : 4 * kPHalf);
-                    const uint32_t fb = mapa_shared(full_bar(stage), 0), dst = base + stage * kPStage;
-                    tma_load_3d_pair(dst + kPHalf, &a.tmap_w, fb, kb * kPK, wr, t.e);
-                    if (!kGather) tma_load_2d_pair(dst, &a.tmap_a, fb, kb * kPK, ar);
+                    __syncwarp();
                     issued |= 1u << stage;
                     issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
                     if (++stage == kPStages) {
@@ -162,9 +165,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             }
             // the even CTA's full barriers count both CTAs' bytes: wait for every phase this
             // CTA issued before the CTA may exit
-            if (rank == 0)
+            if (rank == 0 && leader)
                 for (int s = 0; s < kPStages; ++s)
                     if ((issued & (1u << s)) && !mbar_wait_timed(full_bar(s), (issued_parity >> s) & 1u)) *abort = 1u;
+        } else if (!kGather && warp == 2) {
+            // --------------------------------------------------- producer: rows
+            const bool leader = elect_one();
+            const uint32_t full0 = mapa_shared(full_bar(0), 0);
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = t0; ok && u < tiles; u += dt) {
+                const PTile t = list.at(u);
+                const int ar = t.m0 + 128 * (int)rank;
+                for (int kb = 0; kb < nk; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
+                    if (!ok) break;
+                    if (leader)
+                        tma_load_2d_pair(base + stage * kPStage, &a.tmap_a, full0 + 8u * stage, kb * kPK, ar);
+                    __syncwarp();
+                    if (++stage == kPStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
         } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------------ MMA issuer
             int stage = 0;
@@ -175,15 +200,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             // steps only move the start address (16-byte units, below 2^14), so the issue loop adds
             const uint64_t desc0 = smem_desc_sw128(base, 16, 1024);
             const bool leader = elect_one();
-            for (long long u = t0; ok && u < tiles; u += dt) {
+            for (int u = t0; ok && u < tiles; u += dt) {
                 for (int kb = 0; kb < nk; ++kb, ++it) {
                     const uint32_t b = it & 1u;
-                    ok = mbar_wait_bounded(full_bar(stage), phase, abort) &&
-                         mbar_wait_bounded(tempty_bar(b), ((it >> 1) & 1u) ^ 1u, abort);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort)) &&
+                         __all_sync(0xffffffffu, mbar_wait_bounded(tempty_bar(b), ((it >> 1) & 1u) ^ 1u, abort));
+                    if (!ok) break;
                     tc_fence_after();
                     const uint64_t da = desc0 + (uint32_t)stage * (kPStage >> 4), db = da + (kPHalf >> 4);
                     const uint32_t d = tmem_base + b * kPN;
@@ -211,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (long long u = t0; ok && u < tiles; u += dt)
+            for (int u = t0; ok && u < tiles; u += dt)
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait_bounded(gfull_bar(stage), phase, abort)) {
                         ok = false;
@@ -230,7 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             int slot = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (long long u = t0; ok && u < tiles; u += dt) {
+            for (int u = t0; ok && u < tiles; u += dt) {
                 const PTile t = list.at(u);
                 int srow[4];  // rows of `a`; -1: past the segment or outside `a`, scale 0
 #pragma unroll
@@ -289,13 +311,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
         int slot = 0;
         // a wait that gives up raises the abort flag; the warp then runs on over whatever is there
         // (later waits give up at once), meets the named barriers, and stores nothing
-        for (long long u = t0; u < tiles; u += dt) {
+        for (int u = t0; u < tiles; u += dt) {
             const PTile t = list.at(u);
             float acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0.f;
             for (int kb = 0; kb < nk; kb += 4) {
                 mbar_wait_bounded(sfull_bar(slot), sphase, abort);
+                __syncwarp();
                 float f0[4], f1[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -388,6 +411,7 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     const int n_tiles = (a.N + kPN - 1) / kPN;
     // no more row tiles than P / 256 and one begun per expert
     const int64_t tiles = (a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;  // 32-bit tile numbers in the kernel
     const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
     kernel<<<2 * clusters, p_threads(kGather), PCfg<kMode>::kSmem, s>>>(a);
     return cudaGetLastError();

@@ -48,11 +48,11 @@ struct PTiles {
     const int *off_s, *pre_s;
     int E, N, n_tiles;
     bool concat;
-    __device__ __forceinline__ long long count() const { return (long long)pre_s[E] * n_tiles; }
-    __device__ __forceinline__ PTile at(long long u) const {
+    __device__ __forceinline__ int count() const { return pre_s[E] * n_tiles; }  // below 2^31 (the launch sees to it)
+    __device__ __forceinline__ PTile at(int u) const {
         PTile t;
-        const int mt = (int)(u / n_tiles);
-        t.nt = (int)(u - (long long)mt * n_tiles);
+        const int mt = u / n_tiles;
+        t.nt = u - mt * n_tiles;
         int lo = 0, hi = E - 1;  // largest e with pre_s[e] <= mt
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -134,13 +134,13 @@ __device__ __forceinline__ void store32(const CUtensorMap *map, uint32_t buf, in
 // experts: 358 us like this, 465 with a zero row, 547 with zero fill).
 template <int kStages, typename Empty, typename Gfull>
 __device__ __forceinline__ void gather_rows(const Fp8GemmArgs &a, const PTiles &list, int rank, int g, uint32_t base,
-                                            Empty empty_bar, Gfull gfull_bar, volatile uint32_t *abort, long long t0,
-                                            long long dt) {
+                                            Empty empty_bar, Gfull gfull_bar, volatile uint32_t *abort, int t0,
+                                            int dt) {
     const int piece = g & 7, r0 = g >> 3;
-    const long long tiles = list.count();
+    const int tiles = list.count();
     int stage = 0;
     uint32_t phase = 0;
-    for (long long u = t0; u < tiles; u += dt) {
+    for (int u = t0; u < tiles; u += dt) {
         const PTile t = list.at(u);
         int row[8];  // -1: not copied
 #pragma unroll
