@@ -38,9 +38,11 @@ struct Fp8GemmArgs {
     int32_t E, K, N;
     int32_t nk;                 // ceil(K / 128)
     int32_t layout;             // SwiGlu: MOE_LAYOUT_*
+    int32_t split;              // few-row kernel: CTAs that share a unit's K (set by the launch)
 };
 
 cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);       // picks the kernel
+cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);      // few rows, e8m0
 cudaError_t launch_fp8_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);     // 256-row tiles, any scales
 cudaError_t launch_fp8_mx_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);  // 256-row tiles, e8m0
 

@@ -467,9 +467,10 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     if (a.P == 0 || a.N == 0) return cudaSuccess;
-    // long segments: 256-row tiles on CTA pairs
-    if (a.P > 128ll * a.E)
-        return a.a_f32 || a.w_f32 ? launch_fp8_pair_gemm(mode, a, num_sms, s) : launch_fp8_mx_pair_gemm(mode, a, num_sms, s);
+    const bool e8m0 = !a.a_f32 && !a.w_f32;
+    if (a.P > 128ll * a.E)  // long segments: 256-row tiles on CTA pairs
+        return e8m0 ? launch_fp8_mx_pair_gemm(mode, a, num_sms, s) : launch_fp8_pair_gemm(mode, a, num_sms, s);
+    if (e8m0) return launch_fp8_few_gemm(mode, a, num_sms, s);
     // chunks of 32 rows where the segments hold no more than that on average, else large ones
     const bool few = a.P <= 32ll * a.E;
     if (mode == kFp8SwiGlu)
