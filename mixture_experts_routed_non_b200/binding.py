@@ -885,23 +885,31 @@ def _need_dim(t: torch.Tensor, name: str, dim: int):
 def _need_scale(t: torch.Tensor, name: str, shape, device) -> int:
     if t.dtype not in _SCALE_DTYPES:
         raise TypeError(f"{name}: expected float8_e8m0fnu or float32, got {t.dtype}")
-    _need(t, name, t.dtype, shape, device)
+    _ok(t, name, t.dtype, shape, device)
     return _SCALE_DTYPES[t.dtype]
 
 
-def _new(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """A buffer that belongs to the stream the kernels run on."""
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _ok(t: torch.Tensor, name: str, dtype, shape, device):
+    """_need, with one test where everything is in order (small calls are bound by the host)."""
+    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        _need(t, name, dtype, shape, device)
 
 
-def _given(t: Optional[torch.Tensor], name: str, dtype, shape, device, stream) -> torch.Tensor:
+def _new(like: torch.Tensor, shape, dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A buffer on ``like``'s device that belongs to the stream the kernels run on."""
+    if stream is not None and like.device.type == "cuda":
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=like.device)
+    if like.shape == shape:
+        return torch.empty_like(like, dtype=dtype)
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _given(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     """``t`` checked, or a new buffer."""
     if t is None:
-        return _new(shape, dtype, device, stream)
-    _need(t, name, dtype, shape, device)
+        return _new(like, shape, dtype, stream)
+    _ok(t, name, dtype, shape, like.device)
     return t
 
 
@@ -910,15 +918,20 @@ def _call_on(device, stream: Optional[torch.cuda.Stream], name: str, *args):
     if device.type != "cuda":
         raise ValueError(f"{name}: expected CUDA tensors, got {device}")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        # the handle of torch.cuda.current_stream(device), without making the Stream object
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
-    fn = getattr(load(), name)
+    else:
+        handle = stream.cuda_stream
+    fn = getattr(_lib or load(), name)
     if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream.cuda_stream), name)
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream.cuda_stream), name)
+            status = fn(*args, handle)
+    if status != MOE_OK:
+        raise MoeError(status, name)
 
 
 def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
@@ -935,22 +948,22 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     _need_dim(x, "x", 2)
     N, H = x.shape
     dev = x.device
-    _need(x, "x", torch.bfloat16, (N, H), dev)
-    _need(weight, "weight", torch.bfloat16, (H,), dev)
+    _ok(x, "x", torch.bfloat16, (N, H), dev)
+    _ok(weight, "weight", torch.bfloat16, (H,), dev)
     if not (y or fp8):
         raise ValueError("add_rmsnorm: ask for y, fp8 or both")
     out = out or {}
     r = {}
     if residual is not None:
-        _need(residual, "residual", torch.bfloat16, (N, H), dev)
-        r["res"] = _given(out.get("res"), "res", torch.bfloat16, (N, H), dev, stream)
+        _ok(residual, "residual", torch.bfloat16, (N, H), dev)
+        r["res"] = _given(out.get("res"), "res", x, (N, H), torch.bfloat16, stream)
     if y:
-        r["y"] = _given(out.get("y"), "y", torch.bfloat16, (N, H), dev, stream)
+        r["y"] = _given(out.get("y"), "y", x, (N, H), torch.bfloat16, stream)
     if fp8:
-        r["y8"] = _given(out.get("y8"), "y8", _E4M3, (N, H), dev, stream)
-        r["y8_scale"] = _given(out.get("y8_scale"), "y8_scale", _E8M0, (N, _blocks(H)), dev, stream)
+        r["y8"] = _given(out.get("y8"), "y8", x, (N, H), _E4M3, stream)
+        r["y8_scale"] = _given(out.get("y8_scale"), "y8_scale", x, (N, _blocks(H)), _E8M0, stream)
     if inv_rms:
-        r["inv_rms"] = _given(out.get("inv_rms"), "inv_rms", torch.float32, (N,), dev, stream)
+        r["inv_rms"] = _given(out.get("inv_rms"), "inv_rms", x, (N,), torch.float32, stream)
     for k in out:
         if k not in r:
             raise ValueError(f"out: {k!r} is not written by this call")
@@ -977,18 +990,18 @@ def add_rmsnorm_backward(dy: torch.Tensor, res: torch.Tensor, weight: torch.Tens
     _need_dim(dy, "dy", 2)
     N, H = dy.shape
     dev = dy.device
-    _need(dy, "dy", torch.bfloat16, (N, H), dev)
-    _need(res, "res", torch.bfloat16, (N, H), dev)
-    _need(weight, "weight", torch.bfloat16, (H,), dev)
-    _need(inv_rms, "inv_rms", torch.float32, (N,), dev)
+    _ok(dy, "dy", torch.bfloat16, (N, H), dev)
+    _ok(res, "res", torch.bfloat16, (N, H), dev)
+    _ok(weight, "weight", torch.bfloat16, (H,), dev)
+    _ok(inv_rms, "inv_rms", torch.float32, (N,), dev)
     if dres is not None:
-        _need(dres, "dres", torch.bfloat16, (N, H), dev)
+        _ok(dres, "dres", torch.bfloat16, (N, H), dev)
     grads = grads or {}
-    r = dict(dx=_given(grads.get("dx"), "dx", torch.bfloat16, (N, H), dev, stream),
-             dweight=_given(grads.get("dweight"), "dweight", torch.float32, (H,), dev, stream))
+    r = dict(dx=_given(grads.get("dx"), "dx", dy, (N, H), torch.bfloat16, stream),
+             dweight=_given(grads.get("dweight"), "dweight", dy, (H,), torch.float32, stream))
     if ws is None:
-        ws = _new((add_rmsnorm_backward_workspace_bytes(N, H),), torch.uint8, dev, stream)
-    _need(ws, "ws", torch.uint8, (ws.numel(),), dev)
+        ws = _new(dy, (add_rmsnorm_backward_workspace_bytes(N, H),), torch.uint8, stream)
+    _ok(ws, "ws", torch.uint8, (ws.numel(),), dev)
     _call_on(dev, stream, "moe_add_rmsnorm_backward", dy.data_ptr(), res.data_ptr(), weight.data_ptr(),
              inv_rms.data_ptr(), _ptr(dres), N, H, r["dx"].data_ptr(), r["dweight"].data_ptr(), ws.data_ptr(), ws.numel())
     return r
@@ -1000,9 +1013,9 @@ def quantize_rows_fp8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: 
     _need_dim(x, "x", 2)
     M, K = x.shape
     dev = x.device
-    _need(x, "x", torch.bfloat16, (M, K), dev)
-    q = _given(q, "q", _E4M3, (M, K), dev, stream)
-    scale = _given(scale, "scale", _E8M0, (M, _blocks(K)), dev, stream)
+    _ok(x, "x", torch.bfloat16, (M, K), dev)
+    q = _given(q, "q", x, (M, K), _E4M3, stream)
+    scale = _given(scale, "scale", x, (M, _blocks(K)), _E8M0, stream)
     _call_on(dev, stream, "moe_fp8_quantize_rows", x.data_ptr(), M, K, q.data_ptr(), scale.data_ptr())
     return q, scale
 
@@ -1016,9 +1029,9 @@ def quantize_weight_fp8(w: torch.Tensor, q: Optional[torch.Tensor] = None, scale
     lead = tuple(w.shape[:-2])
     K, N = w.shape[-2:]
     dev = w.device
-    _need(w, "w", torch.bfloat16, w.shape, dev)
-    q = _given(q, "q", _E4M3, lead + (N, K), dev, stream)
-    scale = _given(scale, "scale", _E8M0, lead + (_blocks(N), _blocks(K)), dev, stream)
+    _ok(w, "w", torch.bfloat16, w.shape, dev)
+    q = _given(q, "q", w, lead + (N, K), _E4M3, stream)
+    scale = _given(scale, "scale", w, lead + (_blocks(N), _blocks(K)), _E8M0, stream)
     _call_on(dev, stream, "moe_fp8_quantize_weight", w.data_ptr(), lead[0] if lead else 1, K, N, q.data_ptr(),
              scale.data_ptr())
     return q, scale
@@ -1035,15 +1048,15 @@ def linear_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     M, K = a.shape
     N = w.shape[0]
     dev = a.device
-    _need(a, "a", _E4M3, (M, K), dev)
-    _need(w, "w", _E4M3, (N, K), dev)
+    _ok(a, "a", _E4M3, (M, K), dev)
+    _ok(w, "w", _E4M3, (N, K), dev)
     sa = _need_scale(a_scale, "a_scale", (M, _blocks(K)), dev)
     sw = _need_scale(w_scale, "w_scale", (_blocks(N), _blocks(K)), dev)
     if bias is not None:
-        _need(bias, "bias", torch.bfloat16, (N,), dev)
+        _ok(bias, "bias", torch.bfloat16, (N,), dev)
     if err is not None:
-        _need(err, "err", torch.int32, (1,), dev)
-    out = _given(out, "out", torch.bfloat16, (M, N), dev, stream)
+        _ok(err, "err", torch.int32, (1,), dev)
+    out = _given(out, "out", a, (M, N), torch.bfloat16, stream)
     _call_on(dev, stream, "moe_fp8_linear", a.data_ptr(), a_scale.data_ptr(), sa, M, K, w.data_ptr(),
              w_scale.data_ptr(), sw, N, _ptr(bias), out.data_ptr(), _ptr(err))
     return out
@@ -1065,20 +1078,20 @@ def grouped_linear_fp8(a: torch.Tensor, a_scale: torch.Tensor, expert_off: torch
     rows, K = a.shape
     E, N, _ = w.shape
     dev = a.device
-    _need(a, "a", _E4M3, (rows, K), dev)
-    _need(w, "w", _E4M3, (E, N, K), dev)
+    _ok(a, "a", _E4M3, (rows, K), dev)
+    _ok(w, "w", _E4M3, (E, N, K), dev)
     sa = _need_scale(a_scale, "a_scale", (rows, _blocks(K)), dev)
     sw = _need_scale(w_scale, "w_scale", (E, _blocks(N), _blocks(K)), dev)
-    _need(expert_off, "expert_off", torch.int32, (E + 1,), dev)
+    _ok(expert_off, "expert_off", torch.int32, (E + 1,), dev)
     P = rows
     if gather is not None:
         P = gather.numel()
-        _need(gather, "gather", torch.int32, (P,), dev)
+        _ok(gather, "gather", torch.int32, (P,), dev)
     if bias is not None:
-        _need(bias, "bias", torch.bfloat16, (E, N), dev)
+        _ok(bias, "bias", torch.bfloat16, (E, N), dev)
     if err is not None:
-        _need(err, "err", torch.int32, (1,), dev)
-    out = _given(out, "out", torch.bfloat16, (P, N), dev, stream)
+        _ok(err, "err", torch.int32, (1,), dev)
+    out = _given(out, "out", a, (P, N), torch.bfloat16, stream)
     if P > 0:
         _call_on(dev, stream, "moe_fp8_grouped_linear", a.data_ptr(), a_scale.data_ptr(), sa, rows, K, _ptr(gather), P,
                  expert_off.data_ptr(), E, w.data_ptr(), w_scale.data_ptr(), sw, N, _ptr(bias), out.data_ptr(),
@@ -1112,23 +1125,23 @@ def forward_fp8(x: torch.Tensor, x_scale: torch.Tensor, expert_idx: torch.Tensor
     E, I2, _ = w1.shape
     I = I2 // 2
     dev = x.device
-    _need(x, "x", _E4M3, (N, H), dev)
-    _need(w1, "w1", _E4M3, (E, 2 * I, H), dev)
-    _need(w2, "w2", _E4M3, (E, H, I), dev)
+    _ok(x, "x", _E4M3, (N, H), dev)
+    _ok(w1, "w1", _E4M3, (E, 2 * I, H), dev)
+    _ok(w2, "w2", _E4M3, (E, H, I), dev)
     sx = _need_scale(x_scale, "x_scale", (N, _blocks(H)), dev)
     s1 = _need_scale(w1_scale, "w1_scale", (E, _blocks(2 * I), _blocks(H)), dev)
     s2 = _need_scale(w2_scale, "w2_scale", (E, _blocks(H), _blocks(I)), dev)
     if b1 is not None:
-        _need(b1, "b1", torch.bfloat16, (E, 2 * I), dev)
+        _ok(b1, "b1", torch.bfloat16, (E, 2 * I), dev)
     if b2 is not None:
-        _need(b2, "b2", torch.bfloat16, (E, H), dev)
+        _ok(b2, "b2", torch.bfloat16, (E, H), dev)
     if expert_idx.device != dev:
         raise ValueError(f"expert_idx: expected device {dev}, got {expert_idx.device}")
     r = routing(expert_idx, weights, token_idx=token_idx, N=N, total_pairs=total_pairs)
-    out = _given(out, "out", torch.bfloat16, (N, H), dev, stream)
+    out = _given(out, "out", x, (N, H), torch.bfloat16, stream)
     if ws is None:
-        ws = _new((fp8_workspace_bytes(r, H, I, E),), torch.uint8, dev, stream)
-    _need(ws, "ws", torch.uint8, (ws.numel(),), dev)
+        ws = _new(x, (fp8_workspace_bytes(r, H, I, E),), torch.uint8, stream)
+    _ok(ws, "ws", torch.uint8, (ws.numel(),), dev)
     m = _meta_struct(meta) if meta is not None else None
     _call_on(dev, stream, "moe_fp8_forward", x.data_ptr(), x_scale.data_ptr(), sx, ctypes.byref(r), H, I, E,
              w1.data_ptr(), w1_scale.data_ptr(), s1, _ptr(b1), w2.data_ptr(), w2_scale.data_ptr(), s2, _ptr(b2),

@@ -1,9 +1,9 @@
 // Block-scaled e4m3 products for segments of a few rows, with e8m0 scales on both
 // sides: decode batches and single tokens, bound by reading the weights once.
 //
-// Operands swapped: 128 weight rows on the MMA's M side, a chunk of up to CN rows
-// of `a` on its N side (rounded up to 16), so that a tile's arithmetic follows the
-// few rows there are.  tcgen05.mma.kind::mxf8f6f4.block_scale applies the scales
+// Operands swapped: 128 weight rows on the MMA's M side, a chunk of up to CN = 32
+// (64) rows of `a` on its N side, so that a tile's arithmetic follows the few rows
+// there are (N is always CN: what lies behind the chunk's rows is never read back).  tcgen05.mma.kind::mxf8f6f4.block_scale applies the scales
 // (layout in TMEM: fp8_gemm_mx_sm100.cu) and sums the unit's K in one TMEM
 // accumulator; two accumulators alternate between units.  With SwiGLU a unit has
 // two weight tiles (256 rows: 128 columns of h).
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         const int rem = u - pre_s[lo] * n_tiles;
         FUnit q;
         q.e = lo;
-        q.nt = rem / ch;
+        q.nt = ch == 1 ? rem : rem / ch;
         const int c0 = (rem - q.nt * ch) * CN;
         q.m0 = off_s[lo] + c0;
         q.nv = min(CN, off_s[lo + 1] - q.m0);
@@ -227,21 +227,20 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         // -------------------------------------------------------- MMA issuer
         const bool leader = elect_one();
         const uint64_t desc0 = smem_desc_sw128(base, 16, 1024);  // K-major, 8-row atoms 1024 B apart
+        constexpr uint32_t idesc = idesc_mx_e4m3(kFM, CN);
         int stage = 0;
         uint32_t phase = 0, it = 0;
         bool ok = true;
         for (int u = u0; ok && u < units; u += du, ++it) {
-            const FUnit q = unit_of(u);
-            const uint32_t idesc = idesc_mx_e4m3(kFM, (q.nv + 15) & ~15);
             const uint32_t b = it & 1u, d = tmem_base + b * C::kAcc * CN;
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(tempty_bar(b), ((it >> 1) & 1u) ^ 1u, abort));
             for (int kb = kb0; ok && kb < kb1; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort));
                 if (!ok) break;
                 tc_fence_after();
+                const uint64_t dw = desc0 + (uint32_t)stage * (C::kStage >> 4), dx = dw + (C::kStageW >> 4);
+                const uint32_t sf = tmem_base + C::kScale0 + (uint32_t)stage * C::kScaleCols;
                 if (leader) {
-                    const uint64_t dw = desc0 + (uint32_t)stage * (C::kStage >> 4), dx = dw + (C::kStageW >> 4);
-                    const uint32_t sf = tmem_base + C::kScale0 + (uint32_t)stage * C::kScaleCols;
 #pragma unroll
                     for (int t = 0; t < C::kAcc; ++t)
 #pragma unroll
