@@ -772,6 +772,7 @@ int fp8_forward_impl(const void *x, const void *x_scale, int32_t x_sd, const Rou
         g.err = &ma.hdr->err;
         g.P = r.p_cap;
         g.E = E;
+        g.pdl = 1;
         Fp8GemmArgs up = g;
         up.w = static_cast<const uint8_t *>(w1);
         up.a = static_cast<const uint8_t *>(x);
@@ -806,7 +807,7 @@ int fp8_forward_impl(const void *x, const void *x_scale, int32_t x_sd, const Rou
     }
     if (launch_combine(w + l.y, reinterpret_cast<const int8_t *>(w + l.y_scale), meta.token_offset,
                        meta.s_reverse_scatter_idx, meta.scores, r.N, H, static_cast<__nv_bfloat16 *>(out), ma.hdr,
-                       dev.sms, s, false) != cudaSuccess)
+                       dev.sms, s, r.p_cap > 0) != cudaSuccess)
         return MOE_ERR_CUDA;
     return MOE_OK;
 }

@@ -11,6 +11,10 @@ constexpr int kScaleBlock = 128;  // values along K per scale (rows); 128 x 128 
 inline int scale_blocks(int64_t n) { return (int)((n + kScaleBlock - 1) / kScaleBlock); }
 
 // What the epilogue of a block-scaled product writes.
+// In the forward the products may start as programmatic dependents: the product up
+// (SwiGlu) waits for the metadata before it reads any of it and only then lets the
+// product down (Y16) start, so that one may read the offsets and load weights at
+// once and waits for the product up where it reads h and its scales.
 enum Fp8Mode : int32_t {
     kFp8Bf16 = 0,    // out [P,N] bf16
     kFp8SwiGlu = 1,  // h = silu(gate) up as e4m3 [P,N/2] with an e8m0 scale per 128 columns
@@ -39,6 +43,7 @@ struct Fp8GemmArgs {
     int32_t nk;                 // ceil(K / 128)
     int32_t layout;             // SwiGlu: MOE_LAYOUT_*
     int32_t split;              // few-row kernel: CTAs that share a unit's K (set by the launch)
+    int32_t pdl;                // launched as a programmatic dependent of the launch before it
 };
 
 cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);       // picks the kernel

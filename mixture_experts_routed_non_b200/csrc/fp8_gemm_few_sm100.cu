@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         tmem_alloc(smem_u32(&misc[0]), C::kTmem);
         tmem_relinquish();
     }
+    if (kMode != kFp8Y16) pdl_wait();
+    pdl_launch_dependents();
     load_offsets(a, off_s, kThreads);
     __syncthreads();
     if (warp == 0) {
@@ -205,6 +207,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         }
     } else if (!kGather && warp == 2) {
         // ----------------------------------------------------- producer: rows
+        if (kMode == kFp8Y16) pdl_wait();
         const bool leader = elect_one();
         int stage = 0;
         uint32_t phase = 0;
@@ -285,6 +288,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------ scales
+        if (kMode == kFp8Y16) pdl_wait();
         constexpr int kR = CN / 32;  // rows of `a` per lane
         const int nb = (a.N + 127) / 128, nk = a.nk;
         const uint8_t *as = static_cast<const uint8_t *>(a.a_scale), *ws = static_cast<const uint8_t *>(a.w_scale);
@@ -619,12 +623,18 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     cfg.blockDim = dim3(kGather ? 448 : 384);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)S;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    cfg.numAttrs = S > 1 ? 1 : 0;
+    if (a.pdl) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (S > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = (unsigned)S;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
     return cudaLaunchKernelEx(&cfg, kernel, (const Fp8GemmArgs)a);
 }
 

@@ -71,9 +71,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     using C = XCfg<kMode>;
     constexpr int kPStages = C::kStages, kPThreads = x_threads(kGather);
     extern __shared__ uint8_t smem_raw[];
-    // uniform for both CTAs of the pair: they return together
-    if (a.hdr && *(volatile const uint32_t *)&a.hdr->abort) return;
-
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *base_ptr = smem_raw + (base - raw);
@@ -113,9 +110,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         tmem_alloc_pair(smem_u32(&misc[0]), kPTmem);
         tmem_relinquish_pair();
     }
+    if (kMode != kFp8Y16) pdl_wait();
+    pdl_launch_dependents();
     load_offsets(a, off_s, kPThreads);
     __syncthreads();
-    if (warp == 0) prefix_pieces(off_s, pre_s, E, kPM, lane);
+    if (warp == 0) {
+        prefix_pieces(off_s, pre_s, E, kPM, lane);
+        // nothing to do when the metadata found more pairs than the arrays hold (the same word in
+        // both CTAs of the pair)
+        if (lane == 0 && a.hdr && __ldcg(&a.hdr->abort)) pre_s[E] = 0;
+    }
     tc_fence_before();
     cluster_sync_all();  // barriers of both CTAs initialised before any remote arrive
     tc_fence_after();
@@ -165,6 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
                     if ((issued & (1u << s)) && !mbar_wait_timed(full_bar(s), (issued_parity >> s) & 1u)) *abort = 1u;
         } else if (!kGather && warp == 2) {
             // --------------------------------------------------- producer: rows
+            if (kMode == kFp8Y16) pdl_wait();
             const bool leader = elect_one();
             const uint32_t full0 = mapa_shared(full_bar(0), 0);
             int stage = 0;
@@ -245,6 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     } else if (warp < 8) {
         regs_dec<kXOtherRegs>();
         // ------------------------------------------------------------ scales
+        if (kMode == kFp8Y16) pdl_wait();
         const int nb = (a.N + 127) / 128;
         const uint8_t *as = static_cast<const uint8_t *>(a.a_scale), *ws = static_cast<const uint8_t *>(a.w_scale);
         const uint32_t sf0 = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + kPN;
@@ -414,8 +420,7 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     const int64_t tiles = (a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;  // 32-bit tile numbers in the kernel
     const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
-    kernel<<<2 * clusters, x_threads(kGather), XCfg<kMode>::kSmem, s>>>(a);
-    return cudaGetLastError();
+    return launch_maybe_pdl(kernel, dim3(2 * clusters), dim3(x_threads(kGather)), XCfg<kMode>::kSmem, s, a.pdl != 0, a);
 }
 
 }  // namespace

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kGather ? 256 : 192, 1) fp8_gemm_kernel(const 
     using C = QCfg<CN, kMode>;
     constexpr int kThreads = kGather ? 256 : 192;
     extern __shared__ uint8_t smem_raw[];
+    pdl_wait();  // (its dependents start when it has finished)
     if (a.hdr && *(volatile const uint32_t *)&a.hdr->abort) return;
 
     const uint32_t raw = smem_u32(smem_raw);
@@ -459,8 +460,7 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     const int64_t chunks = a.P / CN + (a.E < a.P ? a.E : a.P);
     const int64_t units = chunks * n_tiles;
     const int ctas = (int)(units < num_sms ? units : num_sms);
-    kernel<<<ctas, kGather ? 256 : 192, C::kSmem, s>>>(a);
-    return cudaGetLastError();
+    return launch_maybe_pdl(kernel, dim3(ctas), dim3(kGather ? 256 : 192), C::kSmem, s, a.pdl != 0, a);
 }
 
 }  // namespace
