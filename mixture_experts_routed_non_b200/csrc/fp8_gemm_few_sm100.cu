@@ -30,6 +30,7 @@ constexpr int kFM = 128;                  // weight rows per MMA
 constexpr uint32_t kFTileW = kFM * kPK;   // 16 KB
 constexpr int kFGather = 64;              // gather threads
 constexpr int kFMaxSplit = 8;
+constexpr int kFSlots = 4;                // scale slots, of four blocks each
 
 template <int CN, int kMode>
 struct FCfg {
@@ -41,12 +42,11 @@ struct FCfg {
     static constexpr int kFit = (int)((200704u - kRed) / kStage);
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr uint32_t kScaleCols = 4 * kAcc + 4;         // weights' scales, then the rows'
-    static constexpr uint32_t kScale0 = 2 * kAcc * CN;           // TMEM column of stage 0's scales
-    static constexpr uint32_t kTmem = kScale0 + kStages * kScaleCols <= 128   ? 128
-                                      : kScale0 + kStages * kScaleCols <= 256 ? 256
-                                                                              : 512;
-    static_assert(kScale0 + kStages * kScaleCols <= 512, "TMEM columns");
-    static constexpr int kBars = 3 * kStages + 7;
+    static constexpr uint32_t kScale0 = 2 * kAcc * CN;           // TMEM column of the first scale slot
+    static constexpr uint32_t kTmemUsed = kScale0 + kFSlots * kScaleCols;
+    static constexpr uint32_t kTmem = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+    static_assert(kTmemUsed <= 512, "TMEM columns");
+    static constexpr int kBars = 3 * kStages + 7 + 2 * kFSlots;
     static constexpr size_t kRedOff = (size_t)kStages * kStage;
     static constexpr size_t kBarOff = kRedOff + kRed;
     static constexpr size_t kMiscOff = kBarOff + 8 * kBars + 8;
@@ -102,6 +102,8 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
     auto tempty_bar = [&](int b) { return bars + 8u * (3 * kStages + 2 + b); };
     const uint32_t drain_bar = bars + 8u * (3 * kStages + 4);
     const uint32_t rfull_bar = drain_bar + 8u, rempty_bar = drain_bar + 16u;
+    auto sfull_bar = [&](int g) { return drain_bar + 8u * (3 + g); };
+    auto sempty_bar = [&](int g) { return drain_bar + 8u * (3 + kFSlots + g); };
     uint32_t *misc = reinterpret_cast<uint32_t *>(base_ptr + C::kMiscOff);
     int *off_s = reinterpret_cast<int *>(base_ptr + C::kTableOff);
     int *pre_s = off_s + (kMaxExperts + 1);
@@ -111,10 +113,13 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            // the producer's arrive (+ TMA bytes), the four scale warps, and the relay
-            mbar_init(full_bar(s), 1 + 4 + (kGather ? 1 : 0));
+            mbar_init(full_bar(s), 1 + (kGather ? 1 : 0));  // the producer's arrive (+ TMA bytes), the relay
             mbar_init(empty_bar(s), 1);
             mbar_init(gfull_bar(s), kFGather);
+        }
+        for (int g = 0; g < kFSlots; ++g) {
+            mbar_init(sfull_bar(g), 4);
+            mbar_init(sempty_bar(g), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
@@ -231,29 +236,38 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         const bool leader = elect_one();
         const uint64_t desc0 = smem_desc_sw128(base, 16, 1024);  // K-major, 8-row atoms 1024 B apart
         constexpr uint32_t idesc = idesc_mx_e4m3(kFM, CN);
-        int stage = 0;
-        uint32_t phase = 0, it = 0;
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, sphase = 0, it = 0;
         bool ok = true;
         for (int u = u0; ok && u < units; u += du, ++it) {
             const uint32_t b = it & 1u, d = tmem_base + b * C::kAcc * CN;
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(tempty_bar(b), ((it >> 1) & 1u) ^ 1u, abort));
             for (int kb = kb0; ok && kb < kb1; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort));
+                const int k = (kb - kb0) & 3;
+                if (k == 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(sfull_bar(slot), sphase, abort));
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort)) && ok;
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t dw = desc0 + (uint32_t)stage * (C::kStage >> 4), dx = dw + (C::kStageW >> 4);
-                const uint32_t sf = tmem_base + C::kScale0 + (uint32_t)stage * C::kScaleCols;
+                const uint32_t sf = tmem_base + C::kScale0 + (uint32_t)slot * C::kScaleCols;
+                const uint32_t id = idesc | idesc_byte(k);
+                const bool group_end = k == 3 || kb == kb1 - 1;
                 if (leader) {
 #pragma unroll
                     for (int t = 0; t < C::kAcc; ++t)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_mx(d + t * CN, dw + t * (kFTileW >> 4) + 2 * kk, dx + 2 * kk, idesc, sf + 4 * t,
+                            umma_mx(d + t * CN, dw + t * (kFTileW >> 4) + 2 * kk, dx + 2 * kk, id, sf + 4 * t,
                                     sf + 4 * C::kAcc, kb > kb0 || kk > 0 ? 1u : 0u);
                     umma_commit(empty_bar(stage));
                     if (kb == kb1 - 1) umma_commit(tfull_bar(b));
+                    if (group_end) umma_commit(sempty_bar(slot));
                 }
                 __syncwarp();
+                if (group_end && ++slot == kFSlots) {
+                    slot = 0;
+                    sphase ^= 1u;
+                }
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1u;
@@ -294,7 +308,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         const uint8_t *as = static_cast<const uint8_t *>(a.a_scale), *ws = static_cast<const uint8_t *>(a.w_scale);
         const int ha = e8m0_rows(as, nk | kb0), hw = e8m0_rows(ws, nk | kb0);
         const uint32_t sf0 = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + C::kScale0;
-        int stage = 0;
+        int slot = 0;
         uint32_t phase = 0;
         // a group of four blocks is loaded while the one before is handed over, a unit's row
         // numbers a unit ahead (fp8_gemm_mx_sm100.cu)
@@ -348,29 +362,21 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
                     load_group(kb0);
                     load_rows(u + 2 * du);
                 }
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort));
+                if (!ok) break;
+                const uint32_t sf = sf0 + (uint32_t)slot * C::kScaleCols;
+                tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (kb + k >= kb1) break;
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
-                    if (!ok) break;
-                    const uint32_t sel = 0x1111u * (uint32_t)k;  // byte k four times
-                    const uint32_t sf = sf0 + (uint32_t)stage * C::kScaleCols;
-                    tc_fence_after();
-#pragma unroll
-                    for (int t = 0; t < C::kAcc; ++t) {
-                        const uint32_t w = __byte_perm(cw[t], 0, sel);
-                        tmem_st_x4(sf + 4 * t, w, w, w, w);
-                    }
-                    const uint32_t x0 = __byte_perm(ca[0], 0, sel), x1 = __byte_perm(ca[kR - 1], 0, sel);
-                    tmem_st_x4(sf + 4 * C::kAcc, x0, x1, x1, x1);  // columns past CN rows: not read
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full_bar(stage));
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                for (int t = 0; t < C::kAcc; ++t) tmem_st_x4(sf + 4 * t, cw[t], cw[t], cw[t], cw[t]);
+                // (columns past the chunk's CN rows are not read)
+                tmem_st_x4(sf + 4 * C::kAcc, ca[0], ca[kR - 1], ca[kR - 1], ca[kR - 1]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull_bar(slot));
+                if (++slot == kFSlots) {
+                    slot = 0;
+                    phase ^= 1u;
                 }
             }
         }

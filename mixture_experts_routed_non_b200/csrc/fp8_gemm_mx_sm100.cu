@@ -8,16 +8,18 @@
 // a tile stays in one TMEM accumulator, and nothing but the two operands and
 // their scales moves per block.
 //
-// Scales in TMEM (one byte of a 32-bit word per K step of 32, all four the same
-// here): row 32 c + l of a 128-row operand in lane l of column c, repeated in each
-// lane quarter -- four columns for a CTA's 128 rows of `a`, eight for the tile's
-// 256 weight rows, which both CTAs hold.  Four scale warps per CTA, one per lane
-// quarter, load the scale bytes ahead and store these columns for each stage.
+// Scales in TMEM: row 32 c + l of a 128-row operand in lane l of column c, repeated
+// in each lane quarter -- four columns for a CTA's 128 rows of `a`, eight for the
+// tile's 256 weight rows, which both CTAs hold.  A 32-bit word carries the scales of
+// four blocks of 128 K; the instruction descriptor names the byte to use.  Four scale
+// warps per CTA, one per lane quarter, load the words of a group of four blocks ahead
+// and store them once per group (a store per block kept the loop of wait, store and
+// arrive as long as a block's MMAs).
 //
-// TMEM: the accumulator (256 columns) and a 16-column scale slot per stage.  A
-// second accumulator does not fit beside them, so the epilogue first takes the
-// whole accumulator into registers (64 per thread) and hands it back; conversion
-// and stores run behind the next tile's MMAs.
+// TMEM: the accumulator (256 columns) and four 16-column scale slots.  A second
+// accumulator does not fit beside them, so the epilogue first takes the whole
+// accumulator into registers (64 per thread) and hands it back; conversion and
+// stores run behind the next tile's MMAs.
 //
 // Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer (even
 // CTA), 2 = TMA of the rows or gather relay (fp8_gemm_pair_sm100.cu), 4-7 = scales, 8-23 = epilogue, 24-27 =
@@ -36,14 +38,15 @@ __host__ __device__ constexpr int x_epi_regs(bool gather) { return gather ? 88 :
 constexpr int kXOtherRegs = 48;
 static_assert(4 * x_epi_regs(true) + 3 * kXOtherRegs <= 7 * 72 && 4 * x_epi_regs(false) + 2 * kXOtherRegs <= 6 * 80,
               "the warpgroups' registers are no more than those of the launch");
-constexpr uint32_t kXScaleCols = 16;  // TMEM columns of a stage's scales: `a` at 0, weights at 8
+constexpr uint32_t kXScaleCols = 16;  // TMEM columns of a scale slot: `a` at 0, weights at 8
+constexpr int kXSlots = 4;            // scale slots, of four blocks each
 
 template <int kMode>
 struct XCfg {
     // 16-bit outputs pass through 32 KB of store buffers; the e4m3 rows of SwiGLU are whole
     // sectors per thread and are stored directly
     static constexpr int kStages = kMode == kFp8SwiGlu ? 6 : 5;
-    static constexpr int kBars = 3 * kStages + 3;
+    static constexpr int kBars = 3 * kStages + 3 + 2 * kXSlots;
     static constexpr size_t kStoreOff = (size_t)kStages * kPStage;
     static constexpr size_t kMaxOff = kStoreOff + (kMode == kFp8SwiGlu ? 0 : kPEpiWarps * kPStore);  // [4][128]
     static constexpr size_t kBarOff = kMaxOff + 4 * 128 * 4;
@@ -51,7 +54,7 @@ struct XCfg {
     static constexpr size_t kTableOff = kMiscOff + 16;
     static constexpr size_t kSmem = 1024 + kTableOff + 2 * (kMaxExperts + 1) * 4;
     static_assert(kSmem <= 232448, "shared memory of one CTA (227 KB)");
-    static_assert(kPN + kStages * kXScaleCols <= kPTmem, "TMEM columns");
+    static_assert(kPN + kXSlots * kXScaleCols <= kPTmem, "TMEM columns");
 };
 
 // D[tmem] (+)= (A * scales) (B * scales), e4m3 in, one e8m0 scale per 32 K of each row, K = 32.
@@ -80,6 +83,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     auto gfull_bar = [&](int s) { return bars + 8u * (2 * kPStages + s); };
     const uint32_t tfull_bar = bars + 8u * (3 * kPStages);
     const uint32_t tempty_bar = tfull_bar + 8u, drain_bar = tfull_bar + 16u;
+    auto sfull_bar = [&](int g) { return drain_bar + 8u * (1 + g); };
+    auto sempty_bar = [&](int g) { return drain_bar + 8u * (1 + kXSlots + g); };
     uint32_t *misc = reinterpret_cast<uint32_t *>(base_ptr + C::kMiscOff);
     int *off_s = reinterpret_cast<int *>(base_ptr + C::kTableOff);
     int *pre_s = off_s + (kMaxExperts + 1);
@@ -90,11 +95,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     const int E = a.E;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPStages; ++s) {
-            // even CTA: the producer's arrive (+ both CTAs' TMA bytes), both CTAs' scale warps and,
-            // with gathered rows, both CTAs' relays
-            mbar_init(full_bar(s), 1 + 8 + (kGather ? 2 : 0));
+            // even CTA: the producer's arrive (+ both CTAs' TMA bytes) and, with gathered rows, both
+            // CTAs' relays
+            mbar_init(full_bar(s), 1 + (kGather ? 2 : 0));
             mbar_init(empty_bar(s), 1);
             mbar_init(gfull_bar(s), kPGather);
+        }
+        for (int g = 0; g < kXSlots; ++g) {
+            mbar_init(sfull_bar(g), 8);  // both CTAs' scale warps
+            mbar_init(sempty_bar(g), 1);
         }
         mbar_init(tfull_bar, 1);
         mbar_init(tempty_bar, 2 * kPEpiWarps);
@@ -193,7 +202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------------ MMA issuer
             int stage = 0;
-            uint32_t phase = 0, tphase = 0;
+            uint32_t phase = 0, tphase = 0, sphase = 0;
+            int slot = 0;
             bool ok = true;
             constexpr uint32_t idesc = idesc_mx_e4m3(kPM, kPN);
             // operand descriptors: K-major, 128-byte rows, 8-row atoms 1024 B apart; stages and K
@@ -203,19 +213,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             for (int u = t0; ok && u < tiles; u += dt, tphase ^= 1u) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(tempty_bar, tphase ^ 1u, abort));
                 for (int kb = 0; ok && kb < nk; ++kb) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort));
+                    if ((kb & 3) == 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(sfull_bar(slot), sphase, abort));
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort)) && ok;
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t da = desc0 + (uint32_t)stage * (kPStage >> 4), db = da + (kPHalf >> 4);
-                    const uint32_t sf = tmem_base + kPN + (uint32_t)stage * kXScaleCols;
+                    const uint32_t sf = tmem_base + kPN + (uint32_t)slot * kXScaleCols;
+                    const uint32_t id = idesc | idesc_byte(kb & 3);
+                    const bool group_end = (kb & 3) == 3 || kb == nk - 1;
                     if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_mx_pair(tmem_base, da + 2 * kk, db + 2 * kk, idesc, sf, sf + 8, (kb | kk) != 0 ? 1u : 0u);
+                            umma_mx_pair(tmem_base, da + 2 * kk, db + 2 * kk, id, sf, sf + 8, (kb | kk) != 0 ? 1u : 0u);
                         umma_commit_pair_mc(empty_bar(stage), 0x3);
                         if (kb == nk - 1) umma_commit_pair_mc(tfull_bar, 0x3);
+                        if (group_end) umma_commit_pair_mc(sempty_bar(slot), 0x3);
                     }
                     __syncwarp();
+                    if (group_end && ++slot == kXSlots) {
+                        slot = 0;
+                        sphase ^= 1u;
+                    }
                     if (++stage == kPStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -254,8 +272,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         const int nb = (a.N + 127) / 128;
         const uint8_t *as = static_cast<const uint8_t *>(a.a_scale), *ws = static_cast<const uint8_t *>(a.w_scale);
         const uint32_t sf0 = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + kPN;
-        const uint32_t full0 = mapa_shared(full_bar(0), 0);
-        int stage = 0;
+        const uint32_t sfull0 = mapa_shared(sfull_bar(0), 0);
+        int slot = 0;
         uint32_t phase = 0;
         // The words of the next four blocks are loaded before the current four are handed over,
         // and a tile's row numbers a tile ahead: a tile's first scales would otherwise be two
@@ -312,27 +330,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
                     load_group(0);
                     load_rows(u + 2 * dt);
                 }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (kb + k >= nk) break;
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
-                    if (!ok) break;
-                    const uint32_t sel = 0x1111u * (uint32_t)k;  // byte k four times
-                    const uint32_t sf = sf0 + (uint32_t)stage * kXScaleCols;
-                    const uint32_t w0 = __byte_perm(cw[0], 0, sel), w1 = __byte_perm(cw[1], 0, sel);
-                    tc_fence_after();
-                    tmem_st_x4(sf, __byte_perm(ca[0], 0, sel), __byte_perm(ca[1], 0, sel), __byte_perm(ca[2], 0, sel),
-                               __byte_perm(ca[3], 0, sel));
-                    tmem_st_x4(sf + 8, w0, w0, w0, w0);
-                    tmem_st_x4(sf + 12, w1, w1, w1, w1);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(full0 + 8u * stage);
-                    if (++stage == kPStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort));
+                if (!ok) break;
+                const uint32_t sf = sf0 + (uint32_t)slot * kXScaleCols;
+                tc_fence_after();
+                tmem_st_x4(sf, ca[0], ca[1], ca[2], ca[3]);
+                tmem_st_x4(sf + 8, cw[0], cw[0], cw[0], cw[0]);
+                tmem_st_x4(sf + 12, cw[1], cw[1], cw[1], cw[1]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(sfull0 + 8u * slot);
+                if (++slot == kXSlots) {
+                    slot = 0;
+                    phase ^= 1u;
                 }
             }
         }

@@ -9,10 +9,12 @@ namespace moe {
 #if defined(__CUDACC__)
 
 // Instruction descriptor, kind::mxf8f6f4: A and B e4m3 (format 0), both K-major, e8m0 scales
-// (bit 23), byte 0 of the scale words (both scale ids 0), M x N.
+// (bit 23), M x N; idesc_byte(k) adds the byte of the scale words to use (bits 4-5 for B,
+// 29-30 for A).
 __host__ __device__ constexpr uint32_t idesc_mx_e4m3(int M, int N) {
     return ((static_cast<uint32_t>(N) >> 3) << 17) | (1u << 23) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
+__host__ __device__ constexpr uint32_t idesc_byte(int k) { return (uint32_t)k << 4 | (uint32_t)k << 29; }
 // 32 lanes x 4 (8) 32-bit TMEM columns from registers.
 __device__ __forceinline__ void tmem_st_x4(uint32_t taddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r0), "r"(r1),
