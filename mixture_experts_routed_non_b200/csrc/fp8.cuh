@@ -47,7 +47,8 @@ struct Fp8GemmArgs {
 };
 
 cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);       // picks the kernel
-cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);      // few rows, e8m0
+// few rows, e8m0; chunk: 32 or 64 rows
+cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int chunk, int num_sms, cudaStream_t s);
 cudaError_t launch_fp8_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);     // 256-row tiles, any scales
 cudaError_t launch_fp8_mx_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);  // 256-row tiles, e8m0
 
@@ -67,11 +68,11 @@ struct NormBwdArgs {
     const float *inv_rms;
     __nv_bfloat16 *dx;
     float *dweight;
-    float *part;  // [norm_bwd_parts(N), H]
+    float *part;  // [norm_bwd_parts(N, H), H]
     int64_t N;
     int32_t H;
 };
-int norm_bwd_parts(int64_t N);
+int norm_bwd_parts(int64_t N, int H);
 cudaError_t launch_add_rmsnorm_backward(const NormBwdArgs &a, cudaStream_t s);
 
 cudaError_t launch_quantize_rows(const __nv_bfloat16 *x, int64_t M, int32_t K, uint8_t *q, uint8_t *scale,
@@ -102,15 +103,9 @@ __device__ __forceinline__ uint32_t e4m3_scale_exp(float amax) {
 __device__ __forceinline__ float scale_of_exp(uint32_t e) { return __uint_as_float(e << 23); }          // 1..254
 __device__ __forceinline__ float inv_scale_of_exp(uint32_t e) { return __uint_as_float((254u - e) << 23); }  // 1..253
 
-// e8m0 byte or fp32 at index i as fp32 (e8m0: 0 is 2^-127, 255 is NaN).
-__device__ __forceinline__ float load_scale(const void *p, int f32, size_t i) {
-    if (f32) return __ldg(static_cast<const float *>(p) + i);
-    const uint32_t b = __ldg(static_cast<const uint8_t *>(p) + i);
-    return __uint_as_float(b == 0 ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
-}
-
-// The same in two steps, for loads that should be in flight together: the raw
-// bits of n scales from index i on, and their values.
+// A scale in two steps, for loads that should be in flight together: the raw bits of
+// n scales (e8m0 bytes or fp32) from index i on (behind `last` more, the last one
+// repeated), and their values (e8m0: 0 is 2^-127, 255 is NaN).
 template <int n>
 __device__ __forceinline__ void load_scale_bits(const void *p, int f32, size_t i, int last, uint32_t (&raw)[n]) {
     if (f32) {

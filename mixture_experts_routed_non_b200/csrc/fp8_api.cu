@@ -10,7 +10,7 @@ using namespace moe;
 namespace {
 
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - (1 << 20);
-constexpr int32_t kMaxNormH = 16384;  // columns one block of 256 threads holds, 64 each
+constexpr int32_t kMaxNormH = 16384;  // columns a block of 512 threads holds, 32 each
 
 bool scale_ok(const void *p, int32_t dtype) {
     return dtype == MOE_SCALE_E8M0 || (dtype == MOE_SCALE_F32 && ptr_aligned(p, 4));
@@ -88,7 +88,7 @@ extern "C" MOE_API int moe_add_rmsnorm(const void *x, const void *residual, cons
 
 extern "C" MOE_API size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t N, int32_t H) {
     if (N < 0 || N >= kMaxRows || H < 8 || H % 8 != 0 || H > kMaxNormH) return 0;
-    return (size_t)norm_bwd_parts(N) * H * sizeof(float);
+    return (size_t)norm_bwd_parts(N, H) * H * sizeof(float);
 }
 
 extern "C" MOE_API int moe_add_rmsnorm_backward(const void *dy, const void *res, const void *weight,

@@ -1,18 +1,9 @@
 // Block-scaled e4m3 products for segments of a few rows, with e8m0 scales on both
 // sides: decode batches and single tokens, bound by reading the weights once.
 //
-// Operands swapped: 128 weight rows on the MMA's M side, a chunk of up to CN = 32
-// (64) rows of `a` on its N side, so that a tile's arithmetic follows the few rows
-// there are (N is always CN: what lies behind the chunk's rows is never read back).  tcgen05.mma.kind::mxf8f6f4.block_scale applies the scales
-// (layout in TMEM: fp8_gemm_mx_sm100.cu) and sums the unit's K in one TMEM
-// accumulator; two accumulators alternate between units.  With SwiGLU a unit has
-// two weight tiles (256 rows: 128 columns of h).
-//
-// Few units: a cluster of S CTAs shares a unit, each taking 1/S of K, so that all
-// SMs pull on memory even when one token meets one matrix.  Each CTA leaves its
-// partial sums in its shared memory; the CTAs then share out the tokens, and each
-// adds the S partial sums of its tokens in rank order (no atomics: the result does
-// not depend on timing) and writes them.
+// tcgen05.mma.kind::mxf8f6f4.block_scale applies the scales (layout in TMEM:
+// fp8_gemm_mx_sm100.cu) and sums the unit's K in one TMEM accumulator; two
+// accumulators alternate between units.  Units, K split and epilogue: fp8_few.cuh.
 //
 // Eight stages of 128 K keep 130 KB or more of weights in flight per SM.
 //
@@ -21,15 +12,12 @@
 // epilogue, 12-13 = row gather (gathered rows only).  Every wait is bounded
 // (common.cuh); one that gives up raises the CTA's abort flag, on which every role
 // runs out without storing, and the error word gets MOE_DEVERR_TIMEOUT.
+#include "fp8_few.cuh"
 #include "fp8_mx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kFM = 128;                  // weight rows per MMA
-constexpr uint32_t kFTileW = kFM * kPK;   // 16 KB
-constexpr int kFGather = 64;              // gather threads
-constexpr int kFMaxSplit = 8;
 constexpr int kFSlots = 4;                // scale slots, of four blocks each
 
 template <int CN, int kMode>
@@ -65,25 +53,6 @@ __device__ __forceinline__ void umma_mx(uint32_t d_tmem, uint64_t a_desc, uint64
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
         : "memory");
 }
-// Cluster-scope release and acquire: shared-memory data handed to another CTA.
-__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(cluster_addr)
-                 : "memory");
-    return v;
-}
-
-struct FUnit {
-    int e, nt, m0, nv;  // expert, weight tile, first sorted position, rows
-};
-
-// kS: K splits (CTAs per cluster).
 template <int CN, int kMode, bool kGather>
 __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const __grid_constant__ Fp8GemmArgs a) {
     using C = FCfg<CN, kMode>;
@@ -161,29 +130,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
     const int u0 = S > 1 ? (int)blockIdx.x / S : (int)blockIdx.x, du = S > 1 ? (int)gridDim.x / S : (int)gridDim.x;
     // this CTA's share of the scale blocks along K
     const int kb0 = (int)((long long)a.nk * rank / S), kb1 = (int)((long long)a.nk * (rank + 1) / S);
-    // unit u: experts in order, inside one its weight tiles, inside a tile its chunks
-    auto unit_of = [&](int u) {
-        int lo = 0, hi = E - 1;  // the expert whose units hold u (empty experts hold none)
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (pre_s[mid] * n_tiles <= u) lo = mid;
-            else hi = mid - 1;
-        }
-        const int ch = pre_s[lo + 1] - pre_s[lo];
-        const int rem = u - pre_s[lo] * n_tiles;
-        FUnit q;
-        q.e = lo;
-        q.nt = ch == 1 ? rem : rem / ch;
-        const int c0 = (rem - q.nt * ch) * CN;
-        q.m0 = off_s[lo] + c0;
-        q.nv = min(CN, off_s[lo + 1] - q.m0);
-        return q;
-    };
-    // first weight row of tile t (0 or 1) of a unit
-    auto wrow = [&](int nt, int t) {
-        if (kMode != kFp8SwiGlu) return nt * kFM;
-        return concat ? t * (a.N / 2) + nt * kFM : nt * 2 * kFM + t * kFM;
-    };
+    const FUnits<CN, kMode> list{off_s, pre_s, E, a.N, n_tiles, concat};
 
     if (warp == 0) {
         // -------------------------------------------------- producer: weights
@@ -192,7 +139,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         uint32_t phase = 0;
         bool ok = true;
         for (int u = u0; ok && u < units; u += du) {
-            const FUnit q = unit_of(u);
+            const FUnit q = list.at(u);
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                 if (!ok) break;
@@ -201,7 +148,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
                     mbar_arrive_expect_tx(fb, C::kStageW + (kGather ? 0u : C::kStageA));
 #pragma unroll
                     for (int t = 0; t < C::kAcc; ++t)
-                        tma_load_3d(dst + t * kFTileW, &a.tmap_w, fb, kb * kPK, wrow(q.nt, t), q.e);
+                        tma_load_3d(dst + t * kFTileW, &a.tmap_w, fb, kb * kPK, list.wrow(q.nt, t), q.e);
                 }
                 __syncwarp();
                 if (++stage == kStages) {
@@ -218,7 +165,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         uint32_t phase = 0;
         bool ok = true;
         for (int u = u0; ok && u < units; u += du) {
-            const FUnit q = unit_of(u);
+            const FUnit q = list.at(u);
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                 if (!ok) break;
@@ -317,7 +264,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         size_t wi[C::kAcc];
         uint32_t ra[kR][2], rw[C::kAcc][2];
         auto load_rows = [&](int u) {
-            if (u < units) q = unit_of(u);
+            if (u < units) q = list.at(u);
 #pragma unroll
             for (int i = 0; i < kR; ++i) {
                 const int j = 32 * i + lane;
@@ -328,7 +275,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
 #pragma unroll
             for (int i = 0; i < kR; ++i) srow[i] = nrow[i] < a.rows ? nrow[i] : -1;
 #pragma unroll
-            for (int t = 0; t < C::kAcc; ++t) wi[t] = ((size_t)q.e * nb + wrow(q.nt, t) / kFM) * nk;
+            for (int t = 0; t < C::kAcc; ++t) wi[t] = ((size_t)q.e * nb + list.wrow(q.nt, t) / kFM) * nk;
         };
         auto load_group = [&](int kb) {
             const int last = kb1 - 1 - kb;
@@ -387,7 +334,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         float *red_s = reinterpret_cast<float *>(base_ptr + C::kRedOff);
         uint32_t it = 0;
         for (int u = u0; u < units; u += du, ++it) {
-            const FUnit q = unit_of(u);
+            const FUnit q = list.at(u);
             const uint32_t b = it & 1u;
             mbar_wait_bounded(tfull_bar(b), (it >> 1) & 1u, abort);
             // the partial sums of the unit before have been read, here and by the peers
@@ -408,172 +355,17 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
                     }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(tempty_bar(b));
-                if (S == 1) mbar_arrive(rfull_bar);
-            }
-            if (S > 1 && lane < S) mbar_arrive_cluster_release(mapa_shared(rfull_bar, lane));
-            mbar_wait_bounded(rfull_bar, it & 1u, abort);
-            if (S > 1) fence_acquire_cluster();
-            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(b));
+            partials_ready(rfull_bar, it & 1u, S, lane, abort);
             const bool ok = *abort == 0;
-
-            // Tokens rank, rank + S, ...: eight at a time, 16 threads each, eight neighbouring
-            // columns per thread.
-            const int c8 = (tid & 15) * 8;
-            for (int j0 = rank; j0 < q.nv; j0 += 8 * S) {
-                const int j = j0 + (tid >> 4) * S;
-                const bool has = j < q.nv;
-                const int jj = has ? j : j0;
-                auto sum8 = [&](int t, int row, float (&v)[8]) {  // weight rows row .. row + 7 of tile t
-                    const uint32_t at = (uint32_t)((t * CN + jj) * kFM + row) * 4u;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                    for (int s = 0; s < S; ++s) {
-                        float4 x, y;
-                        if (S > 1) {
-                            const uint32_t src = mapa_shared(red + at, (uint32_t)s);
-                            x = ld_cluster_f4(src);
-                            y = ld_cluster_f4(src + 16);
-                        } else {
-                            x = *reinterpret_cast<const float4 *>(base_ptr + C::kRedOff + at);
-                            y = *reinterpret_cast<const float4 *>(base_ptr + C::kRedOff + at + 16);
-                        }
-                        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-                        v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-                    }
-                };
-                auto add_bias8 = [&](int col, float (&v)[8]) {
-                    if (!a.bias) return;
-                    const __nv_bfloat16 *br = a.bias + (size_t)q.e * a.N + col;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] += __bfloat162float(br[i]);
-                };
-                const size_t p = (size_t)q.m0 + jj;
-                bool outside = false;  // a gathered row outside `a` counts as zeros
-                if (kGather) {
-                    const int src = __ldg(a.gather + p);
-                    outside = src < 0 || src >= a.rows;
-                }
-                auto keep = [&](float (&v)[8]) {
-                    if (kGather && outside)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                };
-                if (kMode != kFp8SwiGlu) {
-                    const int n = q.nt * kFM + c8;  // N is a multiple of 8: the eight are all inside or all past it
-                    float v[8];
-                    sum8(0, c8, v);
-                    keep(v);
-                    if (n < a.N) add_bias8(n, v);
-                    if (kMode == kFp8Bf16) {
-                        if (ok && has && n < a.N)
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + p * a.N + n) =
-                                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                           pack_bf16x2(v[6], v[7]));
-                    } else {  // fp16 scaled by a power of two per 32 columns: four neighbouring threads
-                        float m = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) m = amax_of(m, v[i]);
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                        const int ex = y_block_exp(m);
-                        const float sc = exp2i(-ex);
-                        if (ok && has) {
-                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + p * a.N + n) =
-                                make_uint4(pack_f16x2(v[0] * sc, v[1] * sc), pack_f16x2(v[2] * sc, v[3] * sc),
-                                           pack_f16x2(v[4] * sc, v[5] * sc), pack_f16x2(v[6] * sc, v[7] * sc));
-                            if ((tid & 3) == 0)
-                                static_cast<int8_t *>(a.out_scale)[p * (a.N / kYBlock) + n / kYBlock] = (int8_t)ex;
-                        }
-                    }
-                } else {
-                    // columns c8 .. c8 + 7 of the unit's 128 of h.  Interleaved: tile c8 / 64 holds
-                    // gate and up of column c in rows 2 (c % 64), 2 (c % 64) + 1; concatenated: tile
-                    // 0 the gates, tile 1 the ups
-                    float g[8], up[8];
-                    if (concat) {
-                        sum8(0, c8, g);
-                        sum8(C::kAcc - 1, c8, up);
-                        keep(g);
-                        keep(up);
-                        add_bias8(q.nt * 128 + c8, g);
-                        add_bias8(a.N / 2 + q.nt * 128 + c8, up);
-                    } else {
-                        float x[8], y[8];
-                        const int t = c8 >> 6, row = 2 * (c8 & 63);
-                        sum8(t, row, x);
-                        sum8(t, row + 8, y);
-                        keep(x);
-                        keep(y);
-                        add_bias8(q.nt * 256 + 2 * c8, x);
-                        add_bias8(q.nt * 256 + 2 * c8 + 8, y);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            g[i] = x[2 * i], up[i] = x[2 * i + 1];
-                            g[4 + i] = y[2 * i], up[4 + i] = y[2 * i + 1];
-                        }
-                    }
-                    float m = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        g[i] = inf_to_nan(__fdividef(g[i], 1.0f + __expf(-g[i])) * up[i]);
-                        m = amax_of(m, g[i]);
-                    }
-#pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    const uint32_t e = e4m3_scale_exp(m);
-                    const float is = inv_scale_of_exp(e);
-                    if (ok && has) {
-                        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + p * (a.N / 2) + q.nt * 128 + c8) =
-                            make_uint2(pack_e4m3x4(g[0] * is, g[1] * is, g[2] * is, g[3] * is),
-                                       pack_e4m3x4(g[4] * is, g[5] * is, g[6] * is, g[7] * is));
-                        if ((tid & 15) == 0)
-                            static_cast<uint8_t *>(a.out_scale)[p * (a.N / 256) + q.nt] = (uint8_t)e;
-                    }
-                }
-            }
-            __syncwarp();
-            if (S == 1) {
-                if (lane == 0) mbar_arrive(rempty_bar);
-            } else if (lane < S) {
-                mbar_arrive_cluster_release(mapa_shared(rempty_bar, lane));
-            }
+            few_output<CN, kMode, kGather>(a, q, rank, S, tid, concat, red, base_ptr + C::kRedOff, ok);
+            partials_read(rempty_bar, S, lane);
         }
     } else if (kGather && warp >= 12) {
         // -------------------------------------------------------- row gather
-        // thread g: 16-byte piece (g & 7) of rows (g >> 3) + 8 i, to row * 128 +
-        // ((piece ^ (row & 7)) << 4) (the 128-byte swizzle); sources as in fp8_pair.cuh
-        const int g = (int)threadIdx.x - 384;
-        const int piece = g & 7, r0 = g >> 3;
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int u = u0; ok && u < units; u += du) {
-            const FUnit q = unit_of(u);
-            int row[CN / 8];  // -1: not copied
-#pragma unroll
-            for (int i = 0; i < CN / 8; ++i)
-                row[i] = r0 + 8 * i < q.nv ? (int)min((long long)max(__ldg(a.gather + q.m0 + r0 + 8 * i), 0),
-                                                      (long long)a.rows - 1)
-                                           : -1;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
-                if (!ok) break;
-                const uint32_t dst =
-                    base + stage * C::kStage + C::kStageW + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
-                const uint8_t *src = a.a + min(kb * kPK + piece * 16, a.K - 16);
-#pragma unroll
-                for (int i = 0; i < CN / 8; ++i)
-                    if (row[i] >= 0) cp_async_16(dst + i * 1024, src + (size_t)row[i] * a.K);
-                cp_async_arrive_noinc(gfull_bar(stage));
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        cp_async_wait_all();
+        gather_chunk_rows<CN, kMode, kStages, C::kStage, C::kStageW>(a, list, units, u0, du, kb0, kb1,
+                                                                     (int)threadIdx.x - 384, base, empty_bar,
+                                                                     gfull_bar, abort);
     }
 
     // ---------------------------------------------------------------- teardown
@@ -602,60 +394,22 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     });
     if (err != cudaSuccess) return err;
-    {
-        const uint64_t dims[3] = {(uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E};
-        const uint64_t strides[2] = {(uint64_t)a.K, (uint64_t)a.K * a.N};
-        const uint32_t box[3] = {kPK, kFM, 1};
-        if (!make_map_u8(&a.tmap_w, a.w, 3, dims, strides, box)) return cudaErrorInvalidValue;
-    }
-    if (!kGather) {
-        const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)a.rows};
-        const uint64_t strides[1] = {(uint64_t)a.K};
-        const uint32_t box[2] = {kPK, CN};
-        if (!make_map_u8(&a.tmap_a, a.a, 2, dims, strides, box)) return cudaErrorInvalidValue;
-    }
-    // no more chunks than P / CN and one begun per expert
-    const int n_tiles = kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM;
-    const int64_t units = (a.P / CN + (a.E < a.P ? a.E : a.P)) * n_tiles;
-    if (units > INT32_MAX / 2) return cudaErrorInvalidValue;  // 32-bit unit numbers in the kernel
-    // Split K while the clusters still fit one to an SM each and keep two groups of four blocks
-    int S = 1;
-    while (S < kFMaxSplit && units * S * 2 <= num_sms && a.nk >= 8 * S) S *= 2;
-    a.split = S;
-    int64_t clusters = num_sms / S;
-    if (clusters > units) clusters = units;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * S));
-    cfg.blockDim = dim3(kGather ? 448 : 384);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    cfg.attrs = attr;
-    if (a.pdl) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (S > 1) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = (unsigned)S;
-        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
-        ++cfg.numAttrs;
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, (const Fp8GemmArgs)a);
+    if (!make_few_maps(a, CN, !kGather)) return cudaErrorInvalidValue;
+    return launch_few(kernel, a, CN, kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM, kGather ? 448 : 384, C::kSmem,
+                      num_sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
-    // chunks of 32 rows where the segments hold no more than that on average
-    const bool few = a.P <= 32ll * a.E;
+cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int chunk, int num_sms, cudaStream_t s) {
+    const bool c32 = chunk == 32;
     if (mode == kFp8SwiGlu)
-        return few ? launch_one<32, kFp8SwiGlu, true>(a, num_sms, s) : launch_one<64, kFp8SwiGlu, true>(a, num_sms, s);
+        return c32 ? launch_one<32, kFp8SwiGlu, true>(a, num_sms, s) : launch_one<64, kFp8SwiGlu, true>(a, num_sms, s);
     if (mode == kFp8Y16)
-        return few ? launch_one<32, kFp8Y16, false>(a, num_sms, s) : launch_one<64, kFp8Y16, false>(a, num_sms, s);
+        return c32 ? launch_one<32, kFp8Y16, false>(a, num_sms, s) : launch_one<64, kFp8Y16, false>(a, num_sms, s);
     if (a.gather)
-        return few ? launch_one<32, kFp8Bf16, true>(a, num_sms, s) : launch_one<64, kFp8Bf16, true>(a, num_sms, s);
-    return few ? launch_one<32, kFp8Bf16, false>(a, num_sms, s) : launch_one<64, kFp8Bf16, false>(a, num_sms, s);
+        return c32 ? launch_one<32, kFp8Bf16, true>(a, num_sms, s) : launch_one<64, kFp8Bf16, true>(a, num_sms, s);
+    return c32 ? launch_one<32, kFp8Bf16, false>(a, num_sms, s) : launch_one<64, kFp8Bf16, false>(a, num_sms, s);
 }
 
 }  // namespace moe
