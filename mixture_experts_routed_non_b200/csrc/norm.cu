@@ -16,6 +16,11 @@
 //   c = (1/H) sum_j w_j dy_j s_j
 //   dx_j = dres_j + inv w_j dy_j - inv^3 c s_j       (the gradient of x and of residual alike)
 //   dw_j = sum over rows of dy_j s_j inv
+//
+// Bound by HBM: one pass, every tensor read or written once.  Measured (rates of
+// the bytes that have to move): 16384 x 2048 with residual, 8-bit out 44 us (5.4
+// TB/s); 8191 x 7168 with residual, bf16 out 79 us (6.0 TB/s); gradient of 16384 x
+// 2048 with dres 49 us (5.4 TB/s), its second kernel included.
 #include "fp8.cuh"
 
 namespace moe {
@@ -32,81 +37,139 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// Sum over the T threads of one row (T = blockDim.x: 16, or a multiple of 32),
-// the same value in each.  red: this row's kNMaxT / 32 floats; a caller that
-// comes again passes another buffer in between, so that one barrier is enough.
+// Sum over the T threads of one row (T = blockDim.x: 16, or a multiple of 32), the
+// same value in each, behind a barrier of the whole block.  red: this row's T / 32
+// floats; a caller that comes again passes another buffer in between.
 __device__ __forceinline__ float row_sum(float v, float *red) {
     const int T = blockDim.x;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (T == 16) return v;
-    v += __shfl_xor_sync(0xffffffffu, v, 16);
-    if (T == 32) return v;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    if (T > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
+    if (T > 32 && (threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
+    if (T <= 32) return v;
     float t = 0.f;
     for (int i = 0; i < T / 32; ++i) t += red[i];
     return t;
 }
 
+// A block's rows on their way in: a ring of stages, each blockDim.y neighbouring rows
+// of kIn tensors (whole rows are contiguous: one bulk copy per tensor), loaded ahead
+// by thread (0, 0).  What the loads need in flight -- several times what two loads per
+// thread can hold -- then costs shared memory instead of registers.
+template <int kIn>
+struct RowRing {
+    const __nv_bfloat16 *src[kIn];
+    uint32_t bars, data;  // shared addresses: a barrier per stage, the stages
+    uint32_t row_bytes, stage_bytes;
+    int64_t N, step;
+    int stages;
+    bool leader;
+    uint32_t *gave_up;
+
+    __device__ __forceinline__ void start(uint32_t smem, int H, int64_t n, int64_t first, int n_stages, uint32_t *flag) {
+        bars = smem;
+        data = smem + 64;
+        row_bytes = (uint32_t)H * 2;
+        stage_bytes = row_bytes * blockDim.y;
+        N = n;
+        step = (int64_t)gridDim.x * blockDim.y;
+        stages = n_stages;
+        leader = threadIdx.x == 0 && threadIdx.y == 0;
+        gave_up = flag;
+        if (leader) {
+            *flag = 0;
+            for (int s = 0; s < stages; ++s) mbar_init(bars + 8 * s, 1);
+            fence_barrier_init();
+        }
+        __syncthreads();
+        if (leader)
+            for (int s = 0; s < stages; ++s) fetch(s, first + s * step);
+    }
+    __device__ __forceinline__ uint32_t at(int stage, int t) const { return data + (stage * kIn + t) * stage_bytes; }
+    // thread (0, 0): load the block's rows from row0 on into a stage that nobody reads any more
+    __device__ __forceinline__ void fetch(int stage, int64_t row0) const {
+        if (row0 >= N) return;
+        const int64_t left = N - row0;
+        const uint32_t bytes = row_bytes * (uint32_t)(left < blockDim.y ? left : blockDim.y);
+        mbar_arrive_expect_tx(bars + 8 * stage, kIn * bytes);
+#pragma unroll
+        for (int t = 0; t < kIn; ++t)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             at(stage, t)),
+                         "l"(reinterpret_cast<const char *>(src[t]) + (size_t)row0 * row_bytes), "r"(bytes),
+                         "r"(bars + 8 * stage)
+                         : "memory");
+    }
+    __device__ __forceinline__ void wait(int stage, uint32_t phase) const {
+        mbar_wait_bounded(bars + 8 * stage, phase, gave_up);
+    }
+    __device__ __forceinline__ uint4 chunk(int stage, int t, int c) const {
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(at(stage, t) + threadIdx.y * row_bytes + (uint32_t)c * 16)
+                     : "memory");
+        return v;
+    }
+};
+
 // Thread (x, y) of a block works on row y of the block's rows, on the 8-column
-// chunks x, x + T, ... (V of them).  A block takes rows until there are none; the
-// next rows' loads are in flight while the current ones are reduced and written.
-template <int V>
-__global__ void __launch_bounds__(kNMaxT) add_rmsnorm_kernel(const NormArgs a) {
+// chunks x, x + T, ... (V of them); a block takes rows until there are none.
+template <int V, bool kResidual>
+__global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a, int stages) {
+    extern __shared__ __align__(128) uint8_t ring_smem[];
     __shared__ float red[2][kNMaxT / 32];
+    __shared__ uint32_t gave_up;
     const int T = blockDim.x, chunks = a.H / 8;
     const int blocks = (a.H + kScaleBlock - 1) / kScaleBlock;
     float *my_red[2] = {red[0] + threadIdx.y * (T / 32), red[1] + threadIdx.y * (T / 32)};
-    uint4 w[V], xv[V], rv[V];
+    int64_t row0 = (int64_t)blockIdx.x * blockDim.y;  // of the block: every thread makes the same turns
+    RowRing<kResidual ? 2 : 1> ring;
+    ring.src[0] = a.x;
+    if (kResidual) ring.src[kResidual ? 1 : 0] = a.residual;
+    ring.start(smem_u32(ring_smem), a.H, a.N, row0, stages, &gave_up);
+    uint4 w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = threadIdx.x + i * T;
         w[i] = c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.weight) + c) : make_uint4(0, 0, 0, 0);
     }
-    auto load = [&](int64_t row) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = threadIdx.x + i * T;
-            const bool in = row < a.N && c < chunks;
-            const size_t at = (size_t)row * a.H + c * 8;
-            xv[i] = in ? *reinterpret_cast<const uint4 *>(a.x + at) : make_uint4(0, 0, 0, 0);
-            if (a.residual) rv[i] = in ? *reinterpret_cast<const uint4 *>(a.residual + at) : make_uint4(0, 0, 0, 0);
-        }
-    };
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    int64_t row0 = (int64_t)blockIdx.x * blockDim.y;  // of the block: every thread makes the same turns
-    load(row0 + threadIdx.y);
-    for (int b = 0; row0 < a.N; row0 += step, b ^= 1) {
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int b = 0; row0 < a.N; row0 += ring.step, b ^= 1) {
         const int64_t row = row0 + threadIdx.y;
         const size_t at0 = (size_t)row * a.H;
+        ring.wait(stage, phase);
         uint4 s[V];
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            const int c = threadIdx.x + i * T;
+            const bool in = row < a.N && c < chunks;
+            s[i] = in ? ring.chunk(stage, 0, c) : make_uint4(0, 0, 0, 0);
             float f[8];
-            s[i] = xv[i];
             unpack8(s[i], f);
-            if (a.residual) {
+            if (kResidual && in) {
                 float r[8];
-                unpack8(rv[i], r);
+                unpack8(ring.chunk(stage, kResidual ? 1 : 0, c), r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] += r[j];
                 s[i] = pack8(f);
                 unpack8(s[i], f);
+                *reinterpret_cast<uint4 *>(a.res + at0 + c * 8) = s[i];
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
         }
-        load(row + step);
-        if (a.residual) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = threadIdx.x + i * T;
-                if (row < a.N && c < chunks) *reinterpret_cast<uint4 *>(a.res + at0 + c * 8) = s[i];
-            }
+        ss = row_sum(ss, my_red[b]);  // and every thread has read the stage
+        if (ring.leader) ring.fetch(stage, row0 + stages * ring.step);
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
         }
-        const float inv = 1.0f / sqrtf(row_sum(ss, my_red[b]) / (float)a.H + a.eps);
+        float inv = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+        if (*(volatile uint32_t *)&gave_up) inv = __uint_as_float(0x7FC00000u);  // a load never came: NaN, not a wrong value
         if (a.inv_rms && threadIdx.x == 0 && row < a.N) a.inv_rms[row] = inv;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -143,16 +206,22 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_kernel(const NormArgs a) {
 
 // The same walk over the rows; each block sums its rows' dw in registers, adds up
 // its row groups and leaves part[block].
-template <int V>
-__global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
-    extern __shared__ float sums[];  // [blockDim.y - 1][H] at the end
+template <int V, bool kDres>
+__global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdArgs a, int stages) {
+    extern __shared__ __align__(128) uint8_t ring_smem[];  // at the end [blockDim.y - 1][H] sums
     __shared__ float red[2][kNMaxT / 32];
+    __shared__ uint32_t gave_up;
     pdl_launch_dependents();
     const int T = blockDim.x, chunks = a.H / 8;
     float *my_red[2] = {red[0] + threadIdx.y * (T / 32), red[1] + threadIdx.y * (T / 32)};
+    int64_t row0 = (int64_t)blockIdx.x * blockDim.y;
+    RowRing<kDres ? 3 : 2> ring;
+    ring.src[0] = a.dy;
+    ring.src[1] = a.res;
+    if (kDres) ring.src[kDres ? 2 : 0] = a.dres;
+    ring.start(smem_u32(ring_smem), a.H, a.N, row0, stages, &gave_up);
     float dw[V][8];
-    uint4 w[V], dv[V], sv[V], gv[V];
-    float ninv = 0.f;
+    uint4 w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = threadIdx.x + i * T;
@@ -160,30 +229,21 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
     }
-    auto load = [&](int64_t row) {
-        ninv = row < a.N ? __ldg(a.inv_rms + row) : 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = threadIdx.x + i * T;
-            const bool in = row < a.N && c < chunks;
-            const size_t at = (size_t)row * a.H + c * 8;
-            dv[i] = in ? *reinterpret_cast<const uint4 *>(a.dy + at) : make_uint4(0, 0, 0, 0);
-            sv[i] = in ? __ldg(reinterpret_cast<const uint4 *>(a.res + at)) : make_uint4(0, 0, 0, 0);
-            if (a.dres) gv[i] = in ? *reinterpret_cast<const uint4 *>(a.dres + at) : make_uint4(0, 0, 0, 0);
-        }
-    };
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    int64_t row0 = (int64_t)blockIdx.x * blockDim.y;
-    load(row0 + threadIdx.y);
-    for (int b = 0; row0 < a.N; row0 += step, b ^= 1) {
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int b = 0; row0 < a.N; row0 += ring.step, b ^= 1) {
         const int64_t row = row0 + threadIdx.y;
-        const float inv = ninv;
+        const float inv = row < a.N ? __ldg(a.inv_rms + row) : 0.f;
+        ring.wait(stage, phase);
         uint4 d[V], s[V], g[V];
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            d[i] = dv[i], s[i] = sv[i];
-            if (a.dres) g[i] = gv[i];
+            const int c = threadIdx.x + i * T;
+            const bool in = row < a.N && c < chunks;
+            d[i] = in ? ring.chunk(stage, 0, c) : make_uint4(0, 0, 0, 0);
+            s[i] = in ? ring.chunk(stage, 1, c) : make_uint4(0, 0, 0, 0);
+            if (kDres) g[i] = in ? ring.chunk(stage, kDres ? 2 : 0, c) : make_uint4(0, 0, 0, 0);
             float fd[8], fs[8], fw[8];
             unpack8(d[i], fd);
             unpack8(s[i], fs);
@@ -194,8 +254,14 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
                 dot = fmaf(fd[j] * fw[j], fs[j], dot);
             }
         }
-        load(row + step);
-        const float k = inv * inv * (row_sum(dot, my_red[b]) / (float)a.H);
+        dot = row_sum(dot, my_red[b]);  // and every thread has read the stage
+        if (ring.leader) ring.fetch(stage, row0 + stages * ring.step);
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        if (*(volatile uint32_t *)&gave_up) dot = __uint_as_float(0x7FC00000u);  // a load never came: NaN, not a wrong value
+        const float k = inv * inv * (dot / (float)a.H);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = threadIdx.x + i * T;
@@ -204,14 +270,18 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
                 unpack8(d[i], fd);
                 unpack8(s[i], fs);
                 unpack8(w[i], fw);
-                if (a.dres) unpack8(g[i], o);
+                if (kDres) unpack8(g[i], o);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] += inv * (fd[j] * fw[j] - fs[j] * k);
                 *reinterpret_cast<uint4 *>(a.dx + (size_t)row * a.H + c * 8) = pack8(o);
             }
         }
     }
+    // (a ring that gave up: dweight NaN as well)
+    const float bad = *(volatile uint32_t *)&gave_up ? __uint_as_float(0x7FC00000u) : 0.f;
     if (blockDim.y > 1) {
+        float *sums = reinterpret_cast<float *>(ring_smem + 64);
+        __syncthreads();  // (no load is in flight: every fetch has been waited for)
         if (threadIdx.y > 0) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -228,9 +298,13 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
     for (int i = 0; i < V; ++i) {
         const int c = threadIdx.x + i * T;
         if (c < chunks) {
-            for (int y = 1; y < (int)blockDim.y; ++y)
+            for (int y = 1; y < (int)blockDim.y; ++y) {
+                const float *sums = reinterpret_cast<const float *>(ring_smem + 64);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) dw[i][j] += sums[(y - 1) * a.H + c * 8 + j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dw[i][j] += bad;
             float4 *p = reinterpret_cast<float4 *>(a.part + (size_t)blockIdx.x * a.H + c * 8);
             p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
             p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
@@ -258,12 +332,20 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float *part, i
     if (x == 0 && blockIdx.x * 32 + g < H) dweight[blockIdx.x * 32 + g] = v;
 }
 
-// Threads per row and chunks per thread: two chunks each where the row has more
-// than one warp's worth (one each kept too little in flight: 16384 x 2048 rows took
-// 48 us against NNN), four past 8192 columns; short rows share a block of about 256
-// threads.
+// Threads per row and chunks per thread: two chunks each where the row has more than
+// one warp's worth, four past 8192 columns; short rows share a block of about 256
+// threads.  Stages of the ring: two to four, about 48 KB a block.
 struct NormShape {
     int V, T, R;
+    int stages(int H, int tensors) const {
+        const int n = (48 << 10) / (R * H * 2 * tensors);
+        return n < 2 ? 2 : n > 4 ? 4 : n;
+    }
+    size_t smem(int H, int tensors) const {
+        const size_t ring = 64 + (size_t)stages(H, tensors) * R * H * 2 * tensors;
+        const size_t sums = 64 + (size_t)(R - 1) * H * 4;  // the gradient's row groups, in the ring's place
+        return ring > sums ? ring : sums;
+    }
 };
 NormShape norm_shape(int H) {
     const int chunks = H / 8;
@@ -274,11 +356,41 @@ NormShape norm_shape(int H) {
     s.R = s.T >= 256 ? 1 : 256 / s.T;
     return s;
 }
-constexpr int kSMThreads = 2048;
-#ifndef BWDB
-#define BWDB 296
-#endif
-constexpr int kBwdBlocks = BWDB;
+constexpr int kBwdBlocks = 296;  // two on each of 148 SMs (148: 64 us for 16384 x 2048 against 49; 592: 54)
+
+template <typename Kernel, typename Args>
+cudaError_t launch_rows(Kernel kernel, const Args &a, const NormShape &n, int tensors, unsigned grid, cudaStream_t s) {
+    int unused = 0;
+    const cudaError_t err = launch_setup_once((const void *)kernel, &unused, [&](int, int *v) -> cudaError_t {
+        *v = 1;
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 << 10);
+    });
+    if (err != cudaSuccess) return err;
+    kernel<<<grid, dim3(n.T, n.R), n.smem(a.H, tensors), s>>>(a, n.stages(a.H, tensors));
+    return cudaGetLastError();
+}
+template <bool kResidual>
+cudaError_t launch_forward(const NormArgs &a, int num_sms, cudaStream_t s) {
+    const NormShape n = norm_shape(a.H);
+    // Four blocks to an SM stay resident.  With a bf16 y as many bytes are written as read, and
+    // a second wave of blocks, which staggers loads and stores, is faster (16384 x 2048 48 us
+    // against 52, 8191 x 7168 79 against 84); with y8 alone it is slower (46 against 44).
+    const int64_t groups = (a.N + n.R - 1) / n.R, room = (int64_t)num_sms * (a.y ? 8 : 4);
+    const unsigned grid = (unsigned)(groups < room ? groups : room);
+    const int in = kResidual ? 2 : 1;
+    if (n.V == 1) return launch_rows(add_rmsnorm_kernel<1, kResidual>, a, n, in, grid, s);
+    if (n.V == 2) return launch_rows(add_rmsnorm_kernel<2, kResidual>, a, n, in, grid, s);
+    return launch_rows(add_rmsnorm_kernel<4, kResidual>, a, n, in, grid, s);
+}
+template <bool kDres>
+cudaError_t launch_backward(const NormBwdArgs &a, cudaStream_t s) {
+    const NormShape n = norm_shape(a.H);
+    const unsigned grid = (unsigned)norm_bwd_parts(a.N, a.H);
+    const int in = kDres ? 3 : 2;
+    if (n.V == 1) return launch_rows(add_rmsnorm_bwd_kernel<1, kDres>, a, n, in, grid, s);
+    if (n.V == 2) return launch_rows(add_rmsnorm_bwd_kernel<2, kDres>, a, n, in, grid, s);
+    return launch_rows(add_rmsnorm_bwd_kernel<4, kDres>, a, n, in, grid, s);
+}
 
 }  // namespace
 
@@ -289,27 +401,14 @@ int norm_bwd_parts(int64_t N, int H) {
 
 cudaError_t launch_add_rmsnorm(const NormArgs &a, int num_sms, cudaStream_t s) {
     if (a.N == 0) return cudaSuccess;
-    const NormShape n = norm_shape(a.H);
-    const int64_t groups = (a.N + n.R - 1) / n.R, room = (int64_t)num_sms * (kSMThreads / (n.T * n.R));
-    const dim3 grid((unsigned)(groups < room ? groups : room)), block(n.T, n.R);
-    if (n.V == 1) add_rmsnorm_kernel<1><<<grid, block, 0, s>>>(a);
-    else if (n.V == 2) add_rmsnorm_kernel<2><<<grid, block, 0, s>>>(a);
-    else add_rmsnorm_kernel<4><<<grid, block, 0, s>>>(a);
-    return cudaGetLastError();
+    return a.residual ? launch_forward<true>(a, num_sms, s) : launch_forward<false>(a, num_sms, s);
 }
 
 cudaError_t launch_add_rmsnorm_backward(const NormBwdArgs &a, cudaStream_t s) {
-    const NormShape n = norm_shape(a.H);
-    const int parts = norm_bwd_parts(a.N, a.H);
-    const dim3 block(n.T, n.R);
-    const size_t smem = (size_t)(n.R - 1) * a.H * sizeof(float);  // rows of at most 255 * 8 columns share a block: < 17 KB
-    if (n.V == 1) add_rmsnorm_bwd_kernel<1><<<parts, block, smem, s>>>(a);
-    else if (n.V == 2) add_rmsnorm_bwd_kernel<2><<<parts, block, smem, s>>>(a);
-    else add_rmsnorm_bwd_kernel<4><<<parts, block, smem, s>>>(a);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = a.dres ? launch_backward<true>(a, s) : launch_backward<false>(a, s);
     if (err != cudaSuccess) return err;
     return launch_maybe_pdl(norm_dweight_kernel, dim3((a.H + 31) / 32), dim3(1024), 0, s, true, (const float *)a.part,
-                            parts, a.H, a.dweight);
+                            norm_bwd_parts(a.N, a.H), a.H, a.dweight);
 }
 
 }  // namespace moe
