@@ -9,6 +9,7 @@ but any call without a built library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -917,15 +918,16 @@ def _call_on(device, stream: Optional[torch.cuda.Stream], name: str, *args):
     """The entry point ``name`` on ``device``'s stream, which is its last argument."""
     if device.type != "cuda":
         raise ValueError(f"{name}: expected CUDA tensors, got {device}")
+    index = device.index
     if stream is None:
         # the handle of torch.cuda.current_stream(device), without making the Stream object
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        handle = torch._C._cuda_getCurrentRawStream(index)
     elif stream.device != device:
         raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
     else:
         handle = stream.cuda_stream
     fn = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == index:  # (there are CUDA tensors: the runtime is initialised)
         status = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -946,32 +948,47 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     ``out`` may hold buffers for any of them; out["res"] may be the residual
     itself."""
     _need_dim(x, "x", 2)
-    N, H = x.shape
+    shape = x.shape
+    N, H = shape
     dev = x.device
-    _ok(x, "x", torch.bfloat16, (N, H), dev)
-    _ok(weight, "weight", torch.bfloat16, (H,), dev)
+    bf16 = torch.bfloat16
+    _ok(x, "x", bf16, shape, dev)
+    _ok(weight, "weight", bf16, (H,), dev)
     if not (y or fp8):
         raise ValueError("add_rmsnorm: ask for y, fp8 or both")
-    out = out or {}
+    given = out.get if out else _nothing
     r = {}
+    p_residual = p_res = p_y = p_y8 = p_scale = p_inv = None
     if residual is not None:
-        _ok(residual, "residual", torch.bfloat16, (N, H), dev)
-        r["res"] = _given(out.get("res"), "res", x, (N, H), torch.bfloat16, stream)
+        _ok(residual, "residual", bf16, shape, dev)
+        p_residual = residual.data_ptr()
+        r["res"] = t = _given(given("res"), "res", x, shape, bf16, stream)
+        p_res = t.data_ptr()
     if y:
-        r["y"] = _given(out.get("y"), "y", x, (N, H), torch.bfloat16, stream)
+        r["y"] = t = _given(given("y"), "y", x, shape, bf16, stream)
+        p_y = t.data_ptr()
     if fp8:
-        r["y8"] = _given(out.get("y8"), "y8", x, (N, H), _E4M3, stream)
-        r["y8_scale"] = _given(out.get("y8_scale"), "y8_scale", x, (N, _blocks(H)), _E8M0, stream)
+        r["y8"] = t = _given(given("y8"), "y8", x, shape, _E4M3, stream)
+        p_y8 = t.data_ptr()
+        r["y8_scale"] = t = _given(given("y8_scale"), "y8_scale", x, (N, (H + 127) // 128), _E8M0, stream)
+        p_scale = t.data_ptr()
     if inv_rms:
-        r["inv_rms"] = _given(out.get("inv_rms"), "inv_rms", x, (N,), torch.float32, stream)
-    for k in out:
-        if k not in r:
-            raise ValueError(f"out: {k!r} is not written by this call")
-    _call_on(dev, stream, "moe_add_rmsnorm", x.data_ptr(), _ptr(residual), weight.data_ptr(), N, H, eps,
-             _ptr(r.get("res")), _ptr(r.get("y")), _ptr(r.get("y8")), _ptr(r.get("y8_scale")), _ptr(r.get("inv_rms")))
+        r["inv_rms"] = t = _given(given("inv_rms"), "inv_rms", x, (N,), torch.float32, stream)
+        p_inv = t.data_ptr()
+    if out:
+        for k in out:
+            if k not in r:
+                raise ValueError(f"out: {k!r} is not written by this call")
+    _call_on(dev, stream, "moe_add_rmsnorm", x.data_ptr(), p_residual, weight.data_ptr(), N, H, eps, p_res, p_y, p_y8,
+             p_scale, p_inv)
     return r
 
 
+def _nothing(key):
+    return None
+
+
+@functools.lru_cache(maxsize=256)
 def add_rmsnorm_backward_workspace_bytes(N: int, H: int) -> int:
     n = load().moe_add_rmsnorm_backward_workspace_bytes(N, H)
     if n == 0:
@@ -996,12 +1013,13 @@ def add_rmsnorm_backward(dy: torch.Tensor, res: torch.Tensor, weight: torch.Tens
     _ok(inv_rms, "inv_rms", torch.float32, (N,), dev)
     if dres is not None:
         _ok(dres, "dres", torch.bfloat16, (N, H), dev)
-    grads = grads or {}
-    r = dict(dx=_given(grads.get("dx"), "dx", dy, (N, H), torch.bfloat16, stream),
-             dweight=_given(grads.get("dweight"), "dweight", dy, (H,), torch.float32, stream))
+    given = grads.get if grads else _nothing
+    r = dict(dx=_given(given("dx"), "dx", dy, (N, H), torch.bfloat16, stream),
+             dweight=_given(given("dweight"), "dweight", dy, (H,), torch.float32, stream))
     if ws is None:
         ws = _new(dy, (add_rmsnorm_backward_workspace_bytes(N, H),), torch.uint8, stream)
-    _ok(ws, "ws", torch.uint8, (ws.numel(),), dev)
+    else:
+        _ok(ws, "ws", torch.uint8, (ws.numel(),), dev)
     _call_on(dev, stream, "moe_add_rmsnorm_backward", dy.data_ptr(), res.data_ptr(), weight.data_ptr(),
              inv_rms.data_ptr(), _ptr(dres), N, H, r["dx"].data_ptr(), r["dweight"].data_ptr(), ws.data_ptr(), ws.numel())
     return r
