@@ -733,9 +733,10 @@ Fp8Layout fp8_layout(const Routing &r, int32_t H, int32_t I, int32_t E) {
     return l;
 }
 
-int check_fp8_dense(int32_t H, int32_t I) {
-    if (H <= 0 || I <= 0 || H % kScaleBlock != 0 || I % kScaleBlock != 0 || I > (1 << 28) || H > (1 << 28))
+int check_fp8_dense(const Routing &r, int32_t H, int32_t I, int32_t E) {
+    if (H <= 0 || I <= 0 || H % kScaleBlock != 0 || I % kScaleBlock != 0 || I > (1 << 27) || H > (1 << 28))
         return MOE_ERR_SHAPE;
+    if (!fp8_sizes_ok(r.p_cap, E, H, 2 * I) || !fp8_sizes_ok(r.p_cap, E, I, H)) return MOE_ERR_SHAPE;
     return MOE_OK;
 }
 
@@ -752,7 +753,7 @@ int fp8_forward_impl(const void *x, const void *x_scale, int32_t x_sd, const Rou
     if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(out, 16) || !aligned(b1, 2) ||
         !aligned(b2, 2) || !sc_ok(x_scale, x_sd) || !sc_ok(w1_scale, w1_sd) || !sc_ok(w2_scale, w2_sd))
         return MOE_ERR_ARG;
-    int st = check_fp8_dense(H, I);
+    int st = check_fp8_dense(r, H, I, E);
     if (st) return st;
     const Fp8Layout l = fp8_layout(r, H, I, E);
     if (!ws || !aligned(ws, kAlign) || ws_bytes < l.total) return MOE_ERR_WS;
@@ -1155,7 +1156,7 @@ extern "C" MOE_API int moe_ep_combine(const moe_ep_sources_t *src, const int32_t
 extern "C" MOE_API size_t moe_fp8_forward_workspace_bytes(const moe_routing_t *routing, int32_t H, int32_t I,
                                                           int32_t E) {
     Routing r;
-    if (routing_from_desc(routing, E, &r) || check_fp8_dense(H, I)) return 0;
+    if (routing_from_desc(routing, E, &r) || check_fp8_dense(r, H, I, E)) return 0;
     return fp8_layout(r, H, I, E).total;
 }
 

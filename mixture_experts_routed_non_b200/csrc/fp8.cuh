@@ -46,6 +46,11 @@ struct Fp8GemmArgs {
     int32_t pdl;                // launched as a programmatic dependent of the launch before it
 };
 
+// Sizes the kernels count in 32 bits and the tensor maps can hold.
+inline bool fp8_sizes_ok(int64_t P, int32_t E, int32_t K, int32_t N) {
+    const int64_t units = (P / 32 + (E < P ? E : P) + 1) * ((N + 127) / 128);
+    return units < INT32_MAX / 2 && (int64_t)K * N < ((int64_t)1 << 39);
+}
 cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);       // picks the kernel
 // few rows, e8m0; chunk: 32 or 64 rows
 cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int chunk, int num_sms, cudaStream_t s);

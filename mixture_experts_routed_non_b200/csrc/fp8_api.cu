@@ -21,6 +21,7 @@ int product(const void *a, const void *a_scale, int32_t a_sd, int64_t rows, int3
             int32_t N, const void *bias, void *out, uint32_t *err_word, moe_stream_t stream) {
     if (P < 0 || P >= kMaxRows || rows < 0 || rows >= kMaxRows || E < 1 || E > kMaxExperts) return MOE_ERR_ARG;
     if (K < 16 || K % 16 != 0 || N < 8 || N % 8 != 0 || K > (1 << 28) || N > (1 << 28)) return MOE_ERR_SHAPE;
+    if (!fp8_sizes_ok(P, E, K, N)) return MOE_ERR_SHAPE;
     if (!w || !w_scale || (P > 0 && !out) || (rows > 0 && (!a || !a_scale))) return MOE_ERR_ARG;
     if (gather ? !ptr_aligned(gather, 4) : P != rows) return MOE_ERR_ARG;
     if (P > 0 && rows == 0) return MOE_ERR_ARG;

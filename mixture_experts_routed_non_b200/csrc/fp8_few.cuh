@@ -277,7 +277,6 @@ inline cudaError_t launch_few(void (*kernel)(Fp8GemmArgs), Fp8GemmArgs &a, int c
     // one segment: its chunks; else no more than P / cn and one begun per expert
     const int64_t chunks = a.expert_off ? a.P / cn + (a.E < a.P ? a.E : a.P) : (a.P + cn - 1) / cn;
     const int64_t units = chunks * n_tiles;
-    if (units > INT32_MAX / 2) return cudaErrorInvalidValue;  // 32-bit unit numbers in the kernel
     // split K while the clusters still fit one CTA to an SM and keep a group of four blocks each
     int S = 1;
     while (S < kFMaxSplit && units * S * 2 <= num_sms && a.nk >= 8 * S) S *= 2;

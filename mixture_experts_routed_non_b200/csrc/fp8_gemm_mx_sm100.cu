@@ -25,7 +25,7 @@
 // CTA), 2 = TMA of the rows or gather relay (fp8_gemm_pair_sm100.cu), 4-7 = scales, 8-23 = epilogue, 24-27 =
 // row gather (gathered rows only).  Registers are moved to the epilogue warps
 // (setmaxnreg: with gathered rows 4 x 88 + 3 x 48 per thread of the seven
-// warpgroups, within the 7 x 72 of the launch; else 4 x 96 + 2 x 48 = 6 x 80).  Every wait
+// warpgroups, within the 7 x 72 of the launch; else 4 x 88 + 2 x 64 = 6 x 80).  Every wait
 // is bounded (common.cuh).
 #include "fp8_mx.cuh"
 
@@ -34,9 +34,9 @@ namespace {
 
 // registers per thread of the launch, of the epilogue warpgroups and of the others
 __host__ __device__ constexpr int x_threads(bool gather) { return gather ? 896 : 768; }
-__host__ __device__ constexpr int x_epi_regs(bool gather) { return gather ? 88 : 96; }
-constexpr int kXOtherRegs = 48;
-static_assert(4 * x_epi_regs(true) + 3 * kXOtherRegs <= 7 * 72 && 4 * x_epi_regs(false) + 2 * kXOtherRegs <= 6 * 80,
+constexpr int kXEpiRegs = 88;
+__host__ __device__ constexpr int x_other_regs(bool gather) { return gather ? 48 : 64; }
+static_assert(4 * kXEpiRegs + 3 * x_other_regs(true) <= 7 * 72 && 4 * kXEpiRegs + 2 * x_other_regs(false) <= 6 * 80,
               "the warpgroups' registers are no more than those of the launch");
 constexpr uint32_t kXScaleCols = 16;  // TMEM columns of a scale slot: `a` at 0, weights at 8
 constexpr int kXSlots = 4;            // scale slots, of four blocks each
@@ -141,7 +141,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     const int tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
 
     if (warp < 4) {
-        regs_dec<kXOtherRegs>();
+        regs_dec<x_other_regs(kGather)>();
         if (warp == 0) {
             // ------------------------------------------------ producer: weights
             const bool leader = elect_one();
@@ -266,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         }
         __syncwarp();
     } else if (warp < 8) {
-        regs_dec<kXOtherRegs>();
+        regs_dec<x_other_regs(kGather)>();
         // ------------------------------------------------------------ scales
         if (kMode == kFp8Y16) pdl_wait();
         const int nb = (a.N + 127) / 128;
@@ -348,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             }
         }
     } else if (warp < 24) {
-        regs_inc<x_epi_regs(kGather)>();
+        regs_inc<kXEpiRegs>();
         // ------------------------------------------------------------ epilogue
         const int q4 = warp & 3, cq = (warp - 8) >> 2;
         const uint32_t buf = base + (uint32_t)C::kStoreOff + (uint32_t)(warp - 8) * kPStore;
@@ -382,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         }
         if (lane == 0) bulk_wait0();  // this warp's stores are complete
     } else {
-        regs_dec<kXOtherRegs>();
+        regs_dec<x_other_regs(kGather)>();
         if (kGather)
             gather_rows<kPStages>(a, list, (int)rank, (int)threadIdx.x - 768, base, empty_bar, gfull_bar, abort, t0, dt);
     }
@@ -429,7 +429,6 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     const int n_tiles = (a.N + kPN - 1) / kPN;
     // no more row tiles than P / 256 and one begun per expert
     const int64_t tiles = (a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
-    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;  // 32-bit tile numbers in the kernel
     const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
     return launch_maybe_pdl(kernel, dim3(2 * clusters), dim3(x_threads(kGather)), XCfg<kMode>::kSmem, s, a.pdl != 0, a);
 }

@@ -5,32 +5,33 @@
 // sixteen epilogue warps (four per TMEM lane quarter, 64 columns each) add it,
 // times sa sw, to 64 fp32 registers per thread while the MMAs of the next block
 // fill the other accumulator.  At the tensor cores' full rate a block takes 512
-// clocks, and an accumulator has to come back within about as much: what an
-// epilogue warp spends there is latency (barrier, TMEM load, arithmetic in
-// turn), which four warps per scheduler hide where two did not.
+// clocks; what bounds it here is the hand-over of an accumulator, about 1200
+// clocks of latency (barrier, TMEM load, arithmetic, barrier, in turn) that four
+// warps per scheduler hide in part (8192 x 7168 x 4096: 240 us = 2.0 PFLOP/s; with
+// eight warps of 128 columns 340, with power-of-two scales, which need none of
+// this, 141).
 //
-// Warp roles (24 warps): 0 = TMA of the weights, 1 = TMEM allocator and MMA
-// issuer (even CTA), 2 = TMA of the rows or gather relay, 3 = scale loader, 4-19 = epilogue, 20-23 = row
-// gather (gathered rows only).  The scale loader runs up to eight blocks ahead
-// and leaves sa sw per row and weight half in shared memory, four blocks per
-// slot, so that no epilogue warp waits for global memory.  The relay turns the
-// gather threads' copies into one arrival on the MMA's barrier, after the proxy
-// fence that the tensor cores' reads of them need.  Registers are moved to the
-// epilogue warps (setmaxnreg: with gathered rows 4 x 104 + 2 x 32 per thread of
-// the six warpgroups, the 6 x 80 of the launch; else 4 x 112 + 32 = 5 x 96).
-// The TMA and MMA warps run converged and elect the issuing lane only around the
-// instructions themselves, so that descriptors stay in uniform registers.
-// Every wait is bounded (common.cuh).
+// Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer (even CTA),
+// 2 = TMA of the rows or gather relay, 3 = scale loader, 4-19 = epilogue, 20-23 =
+// row gather (gathered rows only).  The scale loader runs up to eight blocks ahead
+// and leaves sa sw per row and weight half in shared memory, four blocks per slot,
+// so that no epilogue warp waits for global memory.  The relay turns the gather
+// threads' copies into one arrival on the MMA's barrier, after the proxy fence that
+// the tensor cores' reads of them need.  Registers are moved to the epilogue warps
+// (setmaxnreg: with gathered rows 4 x 104 + 2 x 32 per thread of the six
+// warpgroups, the 6 x 80 of the launch; else 4 x 104 + 64 = 5 x 96).  The TMA and
+// MMA warps run converged and elect the issuing lane only around the instructions
+// themselves.  Every wait is bounded (common.cuh).
 #include "fp8_pair.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kPOtherRegs = 32;
 // registers per thread of the launch and, moved, of the four epilogue warpgroups
 __host__ __device__ constexpr int p_threads(bool gather) { return gather ? 768 : 640; }
-__host__ __device__ constexpr int p_epi_regs(bool gather) { return gather ? 104 : 112; }
-static_assert(4 * 104 + 2 * kPOtherRegs == 6 * 80 && 4 * 112 + kPOtherRegs == 5 * 96,
+__host__ __device__ constexpr int p_epi_regs(bool) { return 104; }
+__host__ __device__ constexpr int p_other_regs(bool gather) { return gather ? 32 : 64; }
+static_assert(4 * p_epi_regs(true) + 2 * p_other_regs(true) == 6 * 80 && 4 * p_epi_regs(false) + p_other_regs(false) == 5 * 96,
               "the warpgroups' registers are those of the launch");
 constexpr int kPSlots = 2;                  // scale slots of four blocks: [4][2 halves][128 rows] fp32
 constexpr uint32_t kPSlot = 4 * 2 * 128;    // floats
@@ -137,7 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
     const int tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
 
     if (warp < 4) {
-        regs_dec<kPOtherRegs>();
+        regs_dec<p_other_regs(kGather)>();
         if (warp == 0) {
             // ------------------------------------------------ producer: weights
             const bool leader = elect_one();
@@ -271,28 +272,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
 #pragma unroll
                 for (int h = 0; h < 2; ++h) wi[h] = ((size_t)t.e * nb + min(list.wrow(t.nt, h) / 128, nb - 1)) * nk;
                 for (int kb = 0; kb < nk; kb += 4) {
-                    uint32_t rw[2][4], ra[4][4];
-                    const int last = nk - 1 - kb;  // blocks behind the end repeat the last one: never used
-                    load_scale_bits(a.w_scale, a.w_f32, wi[0] + kb, last, rw[0]);
-                    load_scale_bits(a.w_scale, a.w_f32, wi[1] + kb, last, rw[1]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        load_scale_bits(a.a_scale, a.a_f32, (size_t)max(srow[i], 0) * nk + kb, last, ra[i]);
-                    bool w = true;
-                    if (lane == 0) w = mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort);
-                    ok = __shfl_sync(0xffffffffu, w, 0);
-                    if (!ok) break;
                     float *sc = scale_s + slot * kPSlot + lane;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float w0 = scale_of_bits(rw[0][k], a.w_f32), w1 = scale_of_bits(rw[1][k], a.w_f32);
+                    for (int k0 = 0; k0 < 4; k0 += 2) {  // two blocks' loads in flight: few registers here
+                        uint32_t rw[2][2], ra[4][2];
+                        const int kk = min(kb + k0, nk - 1), last = nk - 1 - kk;  // behind the end: never used
+                        load_scale_bits(a.w_scale, a.w_f32, wi[0] + kk, last, rw[0]);
+                        load_scale_bits(a.w_scale, a.w_f32, wi[1] + kk, last, rw[1]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float s = srow[i] >= 0 ? scale_of_bits(ra[i][k], a.a_f32) : 0.f;
-                            sc[k * 256 + 32 * i] = s * w0;
-                            sc[k * 256 + 128 + 32 * i] = s * w1;
+                        for (int i = 0; i < 4; ++i)
+                            load_scale_bits(a.a_scale, a.a_f32, (size_t)max(srow[i], 0) * nk + kk, last, ra[i]);
+                        if (k0 == 0) {
+                            bool w = true;
+                            if (lane == 0) w = mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort);
+                            ok = __shfl_sync(0xffffffffu, w, 0);
+                            if (!ok) break;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float w0 = scale_of_bits(rw[0][k], a.w_f32), w1 = scale_of_bits(rw[1][k], a.w_f32);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float s = srow[i] >= 0 ? scale_of_bits(ra[i][k], a.a_f32) : 0.f;
+                                sc[(k0 + k) * 256 + 32 * i] = s * w0;
+                                sc[(k0 + k) * 256 + 128 + 32 * i] = s * w1;
+                            }
                         }
                     }
+                    if (!ok) break;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sfull_bar(slot));
                     if (++slot == kPSlots) {
@@ -370,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
         }
         if (lane == 0) bulk_wait0();  // this warp's stores are complete
     } else {
-        regs_dec<kPOtherRegs>();
+        regs_dec<p_other_regs(kGather)>();
         if (kGather)
             gather_rows<kPStages>(a, list, (int)rank, (int)threadIdx.x - 640, base, empty_bar, gfull_bar, abort, t0, dt);
     }
@@ -417,7 +424,6 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     const int n_tiles = (a.N + kPN - 1) / kPN;
     // no more row tiles than P / 256 and one begun per expert
     const int64_t tiles = (a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
-    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;  // 32-bit tile numbers in the kernel
     const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
     return launch_maybe_pdl(kernel, dim3(2 * clusters), dim3(p_threads(kGather)), PCfg<kMode>::kSmem, s, a.pdl != 0, a);
 }

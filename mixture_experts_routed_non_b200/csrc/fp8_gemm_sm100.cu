@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
     const bool concat = kMode == kFp8SwiGlu && a.layout == MOE_LAYOUT_CONCATENATED;
     const int n_tiles = kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM;
     const FUnits<CN, kMode> list{off_s, pre_s, E, a.N, n_tiles, concat};
-    const int units = (int)misc[3] * n_tiles;  // below 2^31 (the launch sees to it)
+    const int units = (int)misc[3] * n_tiles;  // below 2^31 (fp8_sizes_ok)
     const int u0 = S > 1 ? (int)blockIdx.x / S : (int)blockIdx.x, du = S > 1 ? (int)gridDim.x / S : (int)gridDim.x;
     // this CTA's share of the scale blocks along K
     const int kb0 = (int)((long long)a.nk * rank / S), kb1 = (int)((long long)a.nk * (rank + 1) / S);

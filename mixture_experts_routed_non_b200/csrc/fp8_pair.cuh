@@ -48,7 +48,7 @@ struct PTiles {
     const int *off_s, *pre_s;
     int E, N, n_tiles;
     bool concat;
-    __device__ __forceinline__ int count() const { return pre_s[E] * n_tiles; }  // below 2^31 (the launch sees to it)
+    __device__ __forceinline__ int count() const { return pre_s[E] * n_tiles; }  // below 2^31 (fp8_sizes_ok)
     __device__ __forceinline__ PTile at(int u) const {
         PTile t;
         const int mt = u / n_tiles;

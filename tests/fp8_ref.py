@@ -79,9 +79,12 @@ def make_weight(g, e, n, k, scale, device):
 
 
 def product_noise(nk):
-    """Relative to sum |a||w|: products of e4m3 codes are exact in fp32; at most 128 + nk
-    additions and two scalings, each off by no more than a whole fp32 step."""
-    return (128 + nk + 2) * 2.0 ** -23
+    """Relative to sum |a||w|, for nk blocks of 128: products of e4m3 codes are exact in fp32, and
+    every addition or scaling is off by no more than a whole fp32 step.  Summed block by block: 128
+    additions inside a block, nk of blocks, two scalings.  Summed through (32 values of K per matrix
+    instruction, scales applied to the products): 32 additions inside an instruction, 4 nk of
+    instructions, at most 8 of the K split's parts.  Both stay below 128 + 4 nk."""
+    return (128 + 4 * nk) * 2.0 ** -23
 
 
 def product(a, w, bias=None):

@@ -63,7 +63,7 @@ GROUPED = dict(a=A, a_scale=A, a_sd=0, rows=4, K=256, gather=None, P=4, off=A, E
         (dict(M=-1), ARG), (dict(M=1 << 31), ARG), (dict(K=0), SHAPE), (dict(K=136), SHAPE), (dict(N=0), SHAPE),
         (dict(N=12), SHAPE), (dict(a_sd=2), ARG), (dict(w_sd=-1), ARG), (dict(a=A + 8), ARG), (dict(w=A + 8), ARG),
         (dict(out=A + 2), ARG), (dict(bias=A + 1), ARG), (dict(err=A + 2), ARG), (dict(a_sd=1, a_scale=A + 2), ARG),
-        (dict(w_sd=1, w_scale=A + 1), ARG)]
+        (dict(w_sd=1, w_scale=A + 1), ARG), (dict(K=1 << 20, N=1 << 20), SHAPE), (dict(M=1 << 30, N=1 << 24), SHAPE)]
 ] + [
     ("moe_fp8_grouped_linear", GROUPED, bad, st) for bad, st in [
         (dict(off=None), ARG), (dict(off=A + 2), ARG), (dict(E=0), ARG), (dict(E=1025), ARG), (dict(P=5), ARG),
@@ -98,7 +98,7 @@ def _layer_args(**kw):
     (dict(s2=None), ARG), (dict(out=None), ARG), (dict(xsd=3), ARG), (dict(sd1=2), ARG), (dict(sd2=-1), ARG),
     (dict(act=1), ARG), (dict(lay=2), ARG), (dict(H=192), SHAPE), (dict(I=64), SHAPE), (dict(H=0), SHAPE),
     (dict(x=A + 8), ARG), (dict(w2=A + 4), ARG), (dict(sd1=1, s1=A + 2), ARG), (dict(b1=A + 1), ARG), (dict(ws=None), WS),
-    (dict(ws=A + 128), WS), (dict(wsb=1000), WS), (dict(E=0), ARG), (dict(r=None), ARG)])
+    (dict(ws=A + 128), WS), (dict(wsb=1000), WS), (dict(E=0), ARG), (dict(r=None), ARG), (dict(H=1 << 26, I=1 << 26), SHAPE)])
 def test_layer_refuses(lib, bad, status):
     assert lib.moe_fp8_forward(*_layer_args(**bad)) == status
 

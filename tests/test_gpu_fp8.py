@@ -45,11 +45,38 @@ def test_linear_widths_and_scale_types(K, N, M, sa, sw):
     assert int(err) == 0
 
 
-@pytest.mark.parametrize("M,K,N", [(1500, 512, 1024), (4097, 384, 520), (2048, 2048, 2048)])
-def test_linear_large(M, K, N):
-    a, s, w, t, b = _linear_case(M, K, N, E8, E8, True, M)
+# 256-row tiles: rows of scales that are whole words, half-words and odd bytes; partial tiles
+@pytest.mark.parametrize("M,K,N", [(1500, 512, 4096), (4097, 384, 2056), (2048, 2048, 2048), (3001, 1376, 1096),
+                                   (2500, 768, 2904), (5000, 16, 1288)])
+@pytest.mark.parametrize("sc", [E8, F32])
+def test_linear_large(M, K, N, sc):
+    a, s, w, t, b = _linear_case(M, K, N, sc, sc, True, M)
     y, tol = ref.product(ref.values(a, s), ref.weight_values(w, t), b)
     ref.check(binding.linear_fp8(a, s, w, t, b), y, tol)
+
+
+# K shared out over clusters of 2, 4 and 8, in even and uneven parts
+@pytest.mark.parametrize("K,N", [(1376, 136), (2064, 4096), (4000, 264), (7168, 1024), (11264, 72)])
+@pytest.mark.parametrize("M", [1, 9, 32, 61])
+@pytest.mark.parametrize("sc", [E8, F32])
+def test_linear_split(K, N, M, sc):
+    a, s, w, t, b = _linear_case(M, K, N, sc, sc, M == 9, K + M)
+    y, tol = ref.product(ref.values(a, s), ref.weight_values(w, t), b)
+    out = binding.linear_fp8(a, s, w, t, b)
+    ref.check(out, y, tol)
+    assert torch.equal(out, binding.linear_fp8(a, s, w, t, b))  # the parts are added in a fixed order
+
+
+@pytest.mark.parametrize("M", [3, 2000])
+def test_linear_scales_at_any_address(M):
+    a, s, w, t, _ = _linear_case(M, 1024, 1032, E8, E8, False, 50)
+    want = binding.linear_fp8(a, s, w, t)
+    for shift in (1, 2, 3):
+        def moved(v):
+            buf = torch.empty(v.numel() + 8, dtype=torch.uint8, device="cuda")
+            buf[shift:shift + v.numel()] = v.view(torch.uint8).flatten()
+            return buf[shift:shift + v.numel()].view(E8).view(v.shape)
+        assert torch.equal(binding.linear_fp8(a, moved(s), w, moved(t)), want), shift
 
 
 @pytest.mark.parametrize("M", [1, 40, 700])
@@ -107,6 +134,7 @@ SEGMENTS = {
     "many_small": [i % 5 for i in range(300)],
     "none": [0, 0, 0],
     "long": [2100, 3, 1030],
+    "mid": [10, 64, 65, 0, 33, 20, 63, 1],
 }
 
 
@@ -267,6 +295,7 @@ LAYERS = {
     "rows": (700, 256, 256, 4, 2, 0.2, True, False),
     "skewed": (500, 512, 128, 8, 1, 0.0, False, True),
     "tiles": (1100, 768, 640, 3, 3, 0.05, True, False),
+    "mid": (200, 384, 256, 16, 2, 0.1, True, True),
 }
 
 
@@ -375,6 +404,16 @@ def test_run_together_on_a_stream_and_in_a_graph(N):
         eager = _block(x2, res, *args)
         for k in eager:
             assert torch.equal(cap[k].view(torch.uint8), eager[k].view(torch.uint8)), (seed, k)
+
+
+def test_layer_on_a_given_stream():
+    c = _layer_case(70, 512, 256, 8, 4, 0.1, True, E8, E8, 60)
+    want = binding.forward_fp8(*c)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = [binding.forward_fp8(*c, stream=s) for _ in range(5)]  # workspaces come and go on that stream
+    s.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
 
 
 def test_two_products_on_two_streams():
