@@ -18,8 +18,8 @@
 //   dw_j = sum over rows of dy_j s_j inv
 //
 // Bound by HBM: one pass, every tensor read or written once.  Measured (rates of
-// the bytes that have to move): 16384 x 2048 with residual, 8-bit out 44 us (5.4
-// TB/s); 8191 x 7168 with residual, bf16 out 79 us (6.0 TB/s); gradient of 16384 x
+// the bytes that have to move): 16384 x 2048 with residual, 8-bit out 43 us (5.5
+// TB/s); 8191 x 7168 with residual, bf16 out 78 us (6.0 TB/s); gradient of 16384 x
 // 2048 with dres 49 us (5.4 TB/s), its second kernel included.
 #include "fp8.cuh"
 
@@ -27,6 +27,7 @@ namespace moe {
 namespace {
 
 constexpr int kNMaxT = 512;  // threads per row at most
+constexpr int kStages = 2;   // of the ring (four: 16384 x 2048 55 us against 43, 8191 x 7168 80 against 75)
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
     f[0] = bf16lo(v.x), f[1] = bf16hi(v.x), f[2] = bf16lo(v.y), f[3] = bf16hi(v.y);
@@ -63,33 +64,31 @@ struct RowRing {
     uint32_t bars, data;  // shared addresses: a barrier per stage, the stages
     uint32_t row_bytes, stage_bytes;
     int64_t N, step;
-    int stages;
     bool leader;
     uint32_t *gave_up;
 
-    __device__ __forceinline__ void start(uint32_t smem, int H, int64_t n, int64_t first, int n_stages, uint32_t *flag) {
+    __device__ __forceinline__ void start(uint32_t smem, int H, int64_t n, int64_t first, uint32_t *flag) {
         bars = smem;
         data = smem + 64;
         row_bytes = (uint32_t)H * 2;
         stage_bytes = row_bytes * blockDim.y;
         N = n;
         step = (int64_t)gridDim.x * blockDim.y;
-        stages = n_stages;
         leader = threadIdx.x == 0 && threadIdx.y == 0;
         gave_up = flag;
         if (leader) {
             *flag = 0;
-            for (int s = 0; s < stages; ++s) mbar_init(bars + 8 * s, 1);
+            for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
             fence_barrier_init();
         }
         __syncthreads();
         if (leader)
-            for (int s = 0; s < stages; ++s) fetch(s, first + s * step);
+            for (int s = 0; s < kStages; ++s) fetch(s, first + s * step);
     }
     __device__ __forceinline__ uint32_t at(int stage, int t) const { return data + (stage * kIn + t) * stage_bytes; }
     // thread (0, 0): load the block's rows from row0 on into a stage that nobody reads any more
     __device__ __forceinline__ void fetch(int stage, int64_t row0) const {
-        if (row0 >= N) return;
+        if (row0 >= N || *(volatile uint32_t *)gave_up) return;
         const int64_t left = N - row0;
         const uint32_t bytes = row_bytes * (uint32_t)(left < blockDim.y ? left : blockDim.y);
         mbar_arrive_expect_tx(bars + 8 * stage, kIn * bytes);
@@ -104,6 +103,13 @@ struct RowRing {
     __device__ __forceinline__ void wait(int stage, uint32_t phase) const {
         mbar_wait_bounded(bars + 8 * stage, phase, gave_up);
     }
+    // behind the last row; after a wait that gave up: time for copies in flight to land
+    __device__ __forceinline__ void end() const {
+        if (!*(volatile uint32_t *)gave_up) return;
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+    }
     __device__ __forceinline__ uint4 chunk(int stage, int t, int c) const {
         uint4 v;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -117,7 +123,7 @@ struct RowRing {
 // Thread (x, y) of a block works on row y of the block's rows, on the 8-column
 // chunks x, x + T, ... (V of them); a block takes rows until there are none.
 template <int V, bool kResidual>
-__global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a, int stages) {
+__global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a) {
     extern __shared__ __align__(128) uint8_t ring_smem[];
     __shared__ float red[2][kNMaxT / 32];
     __shared__ uint32_t gave_up;
@@ -128,7 +134,7 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
     RowRing<kResidual ? 2 : 1> ring;
     ring.src[0] = a.x;
     if (kResidual) ring.src[kResidual ? 1 : 0] = a.residual;
-    ring.start(smem_u32(ring_smem), a.H, a.N, row0, stages, &gave_up);
+    ring.start(smem_u32(ring_smem), a.H, a.N, row0, &gave_up);
     uint4 w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -163,8 +169,8 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
             for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
         }
         ss = row_sum(ss, my_red[b]);  // and every thread has read the stage
-        if (ring.leader) ring.fetch(stage, row0 + stages * ring.step);
-        if (++stage == stages) {
+        if (ring.leader) ring.fetch(stage, row0 + kStages * ring.step);
+        if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
         }
@@ -202,12 +208,13 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
             }
         }
     }
+    ring.end();
 }
 
 // The same walk over the rows; each block sums its rows' dw in registers, adds up
 // its row groups and leaves part[block].
 template <int V, bool kDres>
-__global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdArgs a, int stages) {
+__global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
     extern __shared__ __align__(128) uint8_t ring_smem[];  // at the end [blockDim.y - 1][H] sums
     __shared__ float red[2][kNMaxT / 32];
     __shared__ uint32_t gave_up;
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
     ring.src[0] = a.dy;
     ring.src[1] = a.res;
     if (kDres) ring.src[kDres ? 2 : 0] = a.dres;
-    ring.start(smem_u32(ring_smem), a.H, a.N, row0, stages, &gave_up);
+    ring.start(smem_u32(ring_smem), a.H, a.N, row0, &gave_up);
     float dw[V][8];
     uint4 w[V];
 #pragma unroll
@@ -255,8 +262,8 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
             }
         }
         dot = row_sum(dot, my_red[b]);  // and every thread has read the stage
-        if (ring.leader) ring.fetch(stage, row0 + stages * ring.step);
-        if (++stage == stages) {
+        if (ring.leader) ring.fetch(stage, row0 + kStages * ring.step);
+        if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
         }
@@ -277,6 +284,7 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
             }
         }
     }
+    ring.end();
     // (a ring that gave up: dweight NaN as well)
     const float bad = *(volatile uint32_t *)&gave_up ? __uint_as_float(0x7FC00000u) : 0.f;
     if (blockDim.y > 1) {
@@ -334,15 +342,11 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float *part, i
 
 // Threads per row and chunks per thread: two chunks each where the row has more than
 // one warp's worth, four past 8192 columns; short rows share a block of about 256
-// threads.  Stages of the ring: two to four, about 48 KB a block.
+// threads.
 struct NormShape {
     int V, T, R;
-    int stages(int H, int tensors) const {
-        const int n = (48 << 10) / (R * H * 2 * tensors);
-        return n < 2 ? 2 : n > 4 ? 4 : n;
-    }
     size_t smem(int H, int tensors) const {
-        const size_t ring = 64 + (size_t)stages(H, tensors) * R * H * 2 * tensors;
+        const size_t ring = 64 + (size_t)kStages * R * H * 2 * tensors;
         const size_t sums = 64 + (size_t)(R - 1) * H * 4;  // the gradient's row groups, in the ring's place
         return ring > sums ? ring : sums;
     }
@@ -366,7 +370,7 @@ cudaError_t launch_rows(Kernel kernel, const Args &a, const NormShape &n, int te
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 << 10);
     });
     if (err != cudaSuccess) return err;
-    kernel<<<grid, dim3(n.T, n.R), n.smem(a.H, tensors), s>>>(a, n.stages(a.H, tensors));
+    kernel<<<grid, dim3(n.T, n.R), n.smem(a.H, tensors), s>>>(a);
     return cudaGetLastError();
 }
 template <bool kResidual>
