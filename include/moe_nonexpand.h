@@ -579,8 +579,10 @@ MOE_API int moe_fp8_linear(const void *a, const void *a_scale, int32_t a_scale_d
  * int32 ascending (moe_meta_t.expert_frequency_offset), segments of any
  * length, empty ones included; gather [P] int32 (moe_meta_t.x_gather_idx); w
  * [E,N,K], bias [E,N].  Rows of out that no segment covers keep what they
- * held.  Offsets are held inside [0,P]; a gathered row outside [0,rows)
- * counts as zeros (rows >= 1 where P > 0).  Otherwise as moe_fp8_linear; E <= 1024.
+ * held.  Offsets are held inside [0,P], and where they descend a segment is
+ * empty (rows that two segments cover are then left unspecified); a gathered
+ * row outside [0,rows) counts as zeros (rows >= 1 where P > 0).  Otherwise as
+ * moe_fp8_linear; E <= 1024.
  */
 MOE_API int moe_fp8_grouped_linear(const void *a, const void *a_scale, int32_t a_scale_dtype, int64_t rows, int32_t K,
                                    const int32_t *gather, int64_t P, const int32_t *expert_off, int32_t E,

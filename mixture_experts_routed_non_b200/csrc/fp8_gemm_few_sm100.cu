@@ -5,7 +5,10 @@
 // fp8_gemm_mx_sm100.cu) and sums the unit's K in one TMEM accumulator; two
 // accumulators alternate between units.  Units, K split and epilogue: fp8_few.cuh.
 //
-// Eight stages of 128 K keep 130 KB or more of weights in flight per SM.
+// The ring (up to eight stages of 128 K) keeps 112 to 131 KB of weights in flight per
+// SM, 96 KB for SwiGLU in chunks of 64.  1 x 7168 x 4096: 10.5 us, 2.8 TB/s (ramp
+// and join of the split); 1024 skewed rows over 256 experts, K 512, N 2048: 35 us,
+// 72 % of what reading the experts in use costs.
 //
 // Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer, 2 = TMA of
 // the rows or gather relay, 3 idle, 4-7 = scales (one per TMEM lane quarter), 8-11 =
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
     load_offsets(a, off_s, kThreads);
     __syncthreads();
     if (warp == 0) {
-        prefix_pieces(off_s, pre_s, E, CN, lane);
+        prefix_pieces(off_s, pre_s, E, a.P, CN, lane);
         // nothing to do when the metadata found more pairs than the arrays hold
         if (lane == 0) misc[3] = a.hdr && __ldcg(&a.hdr->abort) ? 0u : (uint32_t)pre_s[E];
     }

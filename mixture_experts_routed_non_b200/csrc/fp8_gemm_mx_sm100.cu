@@ -21,6 +21,10 @@
 // accumulator into registers (64 per thread) and hands it back; conversion and
 // stores run behind the next tile's MMAs.
 //
+// Bound by the tensor cores, and in long runs by their power: 8192 x 7168 x 4096 141
+// us (3.4 PFLOP/s), back to back 193; 131072 gathered rows over 128 experts, K 2048,
+// N 1536 367 us (2.2), back to back 469.
+//
 // Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer (even
 // CTA), 2 = TMA of the rows or gather relay (fp8_gemm_pair_sm100.cu), 4-7 = scales, 8-23 = epilogue, 24-27 =
 // row gather (gathered rows only).  Registers are moved to the epilogue warps
@@ -124,7 +128,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     load_offsets(a, off_s, kPThreads);
     __syncthreads();
     if (warp == 0) {
-        prefix_pieces(off_s, pre_s, E, kPM, lane);
+        prefix_pieces(off_s, pre_s, E, a.P, kPM, lane);
         // nothing to do when the metadata found more pairs than the arrays hold (the same word in
         // both CTAs of the pair)
         if (lane == 0 && a.hdr && __ldcg(&a.hdr->abort)) pre_s[E] = 0;

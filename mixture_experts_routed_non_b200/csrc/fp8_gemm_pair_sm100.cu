@@ -121,7 +121,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
     load_offsets(a, off_s, kPThreads);
     __syncthreads();
     if (warp == 0) {
-        prefix_pieces(off_s, pre_s, E, kPM, lane);
+        prefix_pieces(off_s, pre_s, E, a.P, kPM, lane);
         // nothing to do when the metadata found more pairs than the arrays hold (the same word in
         // both CTAs of the pair)
         if (lane == 0 && a.hdr && __ldcg(&a.hdr->abort)) pre_s[E] = 0;

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
     load_offsets(a, off_s, kThreads);
     __syncthreads();
     if (warp == 0) {
-        prefix_pieces(off_s, pre_s, E, CN, lane);
+        prefix_pieces(off_s, pre_s, E, a.P, CN, lane);
         // nothing to do when the metadata found more pairs than the arrays hold
         if (lane == 0) misc[3] = a.hdr && __ldcg(&a.hdr->abort) ? 0u : (uint32_t)pre_s[E];
     }

@@ -79,8 +79,12 @@ __device__ __forceinline__ void load_offsets(const Fp8GemmArgs &a, int *off_s, i
         off_s[threadIdx.x] = threadIdx.x ? (int)a.P : 0;
     }
 }
-// pre_s[e] = pieces of `rows` rows in the experts below e (one converged warp).
-__device__ __forceinline__ void prefix_pieces(const int *off_s, int *pre_s, int E, int rows, int lane) {
+// pre_s[e] = pieces of `rows` rows in the experts below e (one converged warp).  Held at
+// the most that ascending offsets can give: a table that goes up and down would count
+// rows again and again, past what fp8_sizes_ok has bounded.  (No overflow before the
+// minimum: of 32 differences inside [0, P] no more than 16 can be P.)
+__device__ __forceinline__ void prefix_pieces(const int *off_s, int *pre_s, int E, int64_t P, int rows, int lane) {
+    const int most = (int)(P / rows + (E < P ? E : P));
     int sum = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
         const int e = e0 + lane;
@@ -91,8 +95,8 @@ __device__ __forceinline__ void prefix_pieces(const int *off_s, int *pre_s, int 
             const int up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
-        if (e < E) pre_s[e] = sum + incl - n;
-        sum += __shfl_sync(0xffffffffu, incl, 31);
+        if (e < E) pre_s[e] = min(sum + incl - n, most);
+        sum = min(sum + __shfl_sync(0xffffffffu, incl, 31), most);
     }
     if (lane == 0) pre_s[E] = sum;
 }

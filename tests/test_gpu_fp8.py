@@ -213,6 +213,26 @@ def test_grouped_offsets_outside_are_held_inside():
     assert bool((out == 5).all())
 
 
+@pytest.mark.parametrize("rows", [60, 700])
+def test_grouped_rows_before_the_first_segment_and_overlapping_segments(rows):
+    counts = [rows, rows // 2]
+    a, s, off, w, t, b, idx, P = _grouped_case(counts, 256, 128, False, E8, E8, False, 6)
+    want = binding.grouped_linear_fp8(a, s, off, w, t)
+    late = off.clone()
+    late[0] = 9  # the first nine rows belong to nobody
+    out = torch.full_like(want, 5.0)
+    binding.grouped_linear_fp8(a, s, late, w, t, out=out)
+    assert bool((out[:9] == 5).all()) and torch.equal(out[9:], want[9:])
+    # two experts of the same weight claim every row, with an empty segment between: no row is
+    # lost, and none is written outside
+    twice = torch.tensor([0, P, 0, P - 3], dtype=torch.int32, device="cuda")
+    three = [torch.cat([v.view(torch.uint8), v[:1].view(torch.uint8)]).view(v.dtype) for v in (w, t)]
+    out = torch.full_like(want, 5.0)
+    binding.grouped_linear_fp8(a, s, twice, *three, out=out)
+    y, tol = ref.product(ref.values(a, s), ref.weight_values(w[0], t[0]), None)
+    ref.check(out, y, tol)
+
+
 def test_grouped_many_experts():
     rng = np.random.default_rng(0)
     counts = rng.integers(0, 4, 1024).tolist()
