@@ -124,6 +124,7 @@ extern "C" MOE_API int moe_fp8_quantize_rows(const void *x, int64_t M, int32_t K
                                              moe_stream_t stream) {
     if (M < 0 || M >= kMaxRows || (M > 0 && (!x || !q || !scale))) return MOE_ERR_ARG;
     if (K < 16 || K % 16 != 0 || K > (1 << 28)) return MOE_ERR_SHAPE;
+    if (M * scale_blocks(K) >= (int64_t)1 << 36) return MOE_ERR_SHAPE;  // 64 scale blocks to a block of the launch grid
     if (!ptr_aligned(x, 16) || !ptr_aligned(q, 16)) return MOE_ERR_ARG;
     int sms = 0;
     const int st = current_device_sms(&sms);

@@ -52,7 +52,7 @@ GROUPED = dict(a=A, a_scale=A, a_sd=0, rows=4, K=256, gather=None, P=4, off=A, E
 ] + [
     ("moe_fp8_quantize_rows", ROWS, bad, st) for bad, st in [
         (dict(x=None), ARG), (dict(q=None), ARG), (dict(scale=None), ARG), (dict(M=-1), ARG), (dict(K=8), SHAPE),
-        (dict(K=24), SHAPE), (dict(x=A + 2), ARG), (dict(q=A + 8), ARG)]
+        (dict(K=24), SHAPE), (dict(x=A + 2), ARG), (dict(q=A + 8), ARG), (dict(M=1 << 30, K=1 << 28), SHAPE)]
 ] + [
     ("moe_fp8_quantize_weight", WEIGHT, bad, st) for bad, st in [
         (dict(w=None), ARG), (dict(q=None), ARG), (dict(scale=None), ARG), (dict(E=0), ARG), (dict(E=1025), ARG),
