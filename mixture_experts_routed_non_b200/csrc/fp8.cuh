@@ -14,7 +14,8 @@ inline int scale_blocks(int64_t n) { return (int)((n + kScaleBlock - 1) / kScale
 // In the forward the products may start as programmatic dependents: the product up
 // (SwiGlu) waits for the metadata before it reads any of it and only then lets the
 // product down (Y16) start, so that one may read the offsets and load weights at
-// once and waits for the product up where it reads h and its scales.
+// once and waits for the product up where it reads h and its scales.  A product on its
+// own (Bf16) waits before it reads anything: what starts early is its set-up.
 enum Fp8Mode : int32_t {
     kFp8Bf16 = 0,    // out [P,N] bf16
     kFp8SwiGlu = 1,  // h = silu(gate) up as e4m3 [P,N/2] with an e8m0 scale per 128 columns

@@ -52,6 +52,7 @@ int product(const void *a, const void *a_scale, int32_t a_sd, int64_t rows, int3
     g.K = K;
     g.N = N;
     g.nk = scale_blocks(K);
+    g.pdl = 1;
     return launch_fp8_gemm(kFp8Bf16, g, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
                                                                                                       : MOE_ERR_CUDA;
 }

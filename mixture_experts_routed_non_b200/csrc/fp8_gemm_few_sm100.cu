@@ -6,9 +6,9 @@
 // accumulators alternate between units.  Units, K split and epilogue: fp8_few.cuh.
 //
 // The ring (up to eight stages of 128 K) keeps 112 to 131 KB of weights in flight per
-// SM, 96 KB for SwiGLU in chunks of 64.  1 x 7168 x 4096: 10.5 us, 2.8 TB/s (ramp
-// and join of the split); 1024 skewed rows over 256 experts, K 512, N 2048: 35 us,
-// 72 % of what reading the experts in use costs.
+// SM, 96 KB for SwiGLU in chunks of 64.  1 x 7168 x 4096: 9.6 us, 3.1 TB/s (ramp
+// and join of the split); 1024 skewed rows over 256 experts, K 512, N 2048: 32 us,
+// 77 % of what reading the experts in use costs.
 //
 // Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer, 2 = TMA of
 // the rows or gather relay, 3 idle, 4-7 = scales (one per TMEM lane quarter), 8-11 =
@@ -107,10 +107,6 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         tma_prefetch_desc(&a.tmap_w);
         if (!kGather) tma_prefetch_desc(&a.tmap_a);
     }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(&misc[0]), C::kTmem);
-        tmem_relinquish();
-    }
     if (kMode != kFp8Y16) pdl_wait();
     pdl_launch_dependents();
     load_offsets(a, off_s, kThreads);
@@ -118,7 +114,11 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
     if (warp == 0) {
         prefix_pieces(off_s, pre_s, E, a.P, CN, lane);
         // nothing to do when the metadata found more pairs than the arrays hold
-        if (lane == 0) misc[3] = a.hdr && __ldcg(&a.hdr->abort) ? 0u : (uint32_t)pre_s[E];
+        if (lane == 0) misc[3] = a.hdr && load_now(&a.hdr->abort) ? 0u : (uint32_t)pre_s[E];
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&misc[0]), C::kTmem);
+        tmem_relinquish();
     }
     tc_fence_before();
     if (S > 1) cluster_sync_all();  // the peers' barriers are initialised before any remote arrive

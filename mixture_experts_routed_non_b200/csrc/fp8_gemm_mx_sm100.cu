@@ -119,10 +119,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         tma_prefetch_desc(&a.tmap_w);
         if (!kGather) tma_prefetch_desc(&a.tmap_a);
     }
-    if (warp == 1) {
-        tmem_alloc_pair(smem_u32(&misc[0]), kPTmem);
-        tmem_relinquish_pair();
-    }
     if (kMode != kFp8Y16) pdl_wait();
     pdl_launch_dependents();
     load_offsets(a, off_s, kPThreads);
@@ -131,7 +127,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         prefix_pieces(off_s, pre_s, E, a.P, kPM, lane);
         // nothing to do when the metadata found more pairs than the arrays hold (the same word in
         // both CTAs of the pair)
-        if (lane == 0 && a.hdr && __ldcg(&a.hdr->abort)) pre_s[E] = 0;
+        if (lane == 0 && a.hdr && load_now(&a.hdr->abort)) pre_s[E] = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&misc[0]), kPTmem);
+        tmem_relinquish_pair();
     }
     tc_fence_before();
     cluster_sync_all();  // barriers of both CTAs initialised before any remote arrive

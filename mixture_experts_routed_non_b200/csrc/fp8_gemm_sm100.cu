@@ -97,10 +97,6 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
         tma_prefetch_desc(&a.tmap_w);
         if (!kGather) tma_prefetch_desc(&a.tmap_a);
     }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(&misc[0]), C::kTmem);
-        tmem_relinquish();
-    }
     if (kMode != kFp8Y16) pdl_wait();
     pdl_launch_dependents();
     load_offsets(a, off_s, kThreads);
@@ -108,7 +104,11 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
     if (warp == 0) {
         prefix_pieces(off_s, pre_s, E, a.P, CN, lane);
         // nothing to do when the metadata found more pairs than the arrays hold
-        if (lane == 0) misc[3] = a.hdr && __ldcg(&a.hdr->abort) ? 0u : (uint32_t)pre_s[E];
+        if (lane == 0) misc[3] = a.hdr && load_now(&a.hdr->abort) ? 0u : (uint32_t)pre_s[E];
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&misc[0]), C::kTmem);
+        tmem_relinquish();
     }
     tc_fence_before();
     if (S > 1) cluster_sync_all();  // the peers' barriers are initialised before any remote arrive

@@ -70,11 +70,20 @@ struct PTiles {
     }
 };
 
+// A load that stays behind the wait for the kernel before (the read-only loads may be moved
+// ahead of it by the compiler).
+template <typename T>
+__device__ __forceinline__ T load_now(const T *p) {
+    static_assert(sizeof(T) == 4, "a 32-bit word");
+    T v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 // Segment offsets into off_s, held inside [0, P] whatever the caller's table says.
 __device__ __forceinline__ void load_offsets(const Fp8GemmArgs &a, int *off_s, int threads) {
     if (a.expert_off) {
         for (int i = threadIdx.x; i <= a.E; i += threads)
-            off_s[i] = (int)min(max((long long)__ldcg(a.expert_off + i), 0ll), (long long)a.P);
+            off_s[i] = (int)min(max((long long)load_now(a.expert_off + i), 0ll), (long long)a.P);
     } else if (threadIdx.x < 2) {
         off_s[threadIdx.x] = threadIdx.x ? (int)a.P : 0;
     }

@@ -24,6 +24,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __nv_bfloat16 
                                                             uint8_t *scale) {
     const int sub = threadIdx.x & 15;
     const int64_t b0 = (int64_t)blockIdx.x * (16 * kRowsU) + (threadIdx.x >> 4);
+    pdl_wait();
+    pdl_launch_dependents();
     const bool whole = nk * kScaleBlock == K;  // then block b starts at value 128 b
     size_t at[kRowsU];
     uint4 v[kRowsU];
@@ -40,7 +42,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __nv_bfloat16 
             in[i] = in[i] && k < K;
             at[i] = (size_t)row * K + k;
         }
-        v[i] = in[i] ? __ldg(reinterpret_cast<const uint4 *>(x + at[i])) : make_uint4(0, 0, 0, 0);
+        v[i] = in[i] ? *reinterpret_cast<const uint4 *>(x + at[i]) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < kRowsU; ++i) {
@@ -129,8 +131,7 @@ cudaError_t launch_quantize_rows(const __nv_bfloat16 *x, int64_t M, int32_t K, u
     const int nk = scale_blocks(K);
     const int64_t n = M * nk, ctas = (n + 16 * kRowsU - 1) / (16 * kRowsU);
     if (ctas == 0) return cudaSuccess;
-    quantize_rows_kernel<<<(unsigned)ctas, 256, 0, s>>>(x, n, K, nk, q, scale);
-    return cudaGetLastError();
+    return launch_maybe_pdl(quantize_rows_kernel, dim3((unsigned)ctas), dim3(256), 0, s, true, x, n, K, nk, q, scale);
 }
 
 cudaError_t launch_quantize_weight(const __nv_bfloat16 *w, int32_t E, int32_t K, int32_t N, uint8_t *q,

@@ -17,10 +17,12 @@
 //   dx_j = dres_j + inv w_j dy_j - inv^3 c s_j       (the gradient of x and of residual alike)
 //   dw_j = sum over rows of dy_j s_j inv
 //
-// Bound by HBM: one pass, every tensor read or written once.  Measured (rates of
-// the bytes that have to move): 16384 x 2048 with residual, 8-bit out 43 us (5.5
-// TB/s); 8191 x 7168 with residual, bf16 out 78 us (6.0 TB/s); gradient of 16384 x
-// 2048 with dres 49 us (5.4 TB/s), its second kernel included.
+// Bound by HBM: one pass, every tensor read or written once.  Every kernel is a
+// programmatic dependent of the launch before it: its blocks come up and set their
+// barriers while that one ends.  Measured back to back (rates of the bytes that have
+// to move): 16384 x 2048 with residual, 8-bit out 44 us (5.4 TB/s; 45 without the early
+// start); 8191 x 7168 with residual, bf16 out 77 us (6.1 TB/s; 79); gradient of 16384
+// x 2048 with dres 48 us (5.6 TB/s; 49), its second kernel included.
 #include "fp8.cuh"
 
 namespace moe {
@@ -82,6 +84,8 @@ struct RowRing {
             fence_barrier_init();
         }
         __syncthreads();
+        pdl_wait();  // nothing is read or written before
+        pdl_launch_dependents();
         if (leader)
             for (int s = 0; s < kStages; ++s) fetch(s, first + s * step);
     }
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = threadIdx.x + i * T;
-        w[i] = c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.weight) + c) : make_uint4(0, 0, 0, 0);
+        w[i] = c < chunks ? reinterpret_cast<const uint4 *>(a.weight)[c] : make_uint4(0, 0, 0, 0);
     }
     int stage = 0;
     uint32_t phase = 0;
@@ -218,7 +222,6 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
     extern __shared__ __align__(128) uint8_t ring_smem[];  // at the end [blockDim.y - 1][H] sums
     __shared__ float red[2][kNMaxT / 32];
     __shared__ uint32_t gave_up;
-    pdl_launch_dependents();
     const int T = blockDim.x, chunks = a.H / 8;
     float *my_red[2] = {red[0] + threadIdx.y * (T / 32), red[1] + threadIdx.y * (T / 32)};
     int64_t row0 = (int64_t)blockIdx.x * blockDim.y;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = threadIdx.x + i * T;
-        w[i] = c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.weight) + c) : make_uint4(0, 0, 0, 0);
+        w[i] = c < chunks ? reinterpret_cast<const uint4 *>(a.weight)[c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
     }
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
     uint32_t phase = 0;
     for (int b = 0; row0 < a.N; row0 += ring.step, b ^= 1) {
         const int64_t row = row0 + threadIdx.y;
-        const float inv = row < a.N ? __ldg(a.inv_rms + row) : 0.f;
+        const float inv = row < a.N ? a.inv_rms[row] : 0.f;
         ring.wait(stage, phase);
         uint4 d[V], s[V], g[V];
         float dot = 0.f;
@@ -326,6 +329,7 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float *part, i
     __shared__ float sm[32][33];
     const int x = threadIdx.x & 31, g = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     pdl_wait();
+    pdl_launch_dependents();
     float v = 0.f;
     if (c < H) {
 #pragma unroll 4
@@ -370,8 +374,7 @@ cudaError_t launch_rows(Kernel kernel, const Args &a, const NormShape &n, int te
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 << 10);
     });
     if (err != cudaSuccess) return err;
-    kernel<<<grid, dim3(n.T, n.R), n.smem(a.H, tensors), s>>>(a);
-    return cudaGetLastError();
+    return launch_maybe_pdl(kernel, dim3(grid), dim3(n.T, n.R), n.smem(a.H, tensors), s, true, a);
 }
 template <bool kResidual>
 cudaError_t launch_forward(const NormArgs &a, int num_sms, cudaStream_t s) {

@@ -448,3 +448,58 @@ def test_two_products_on_two_streams():
     torch.cuda.synchronize()
     for o, o2 in outs:
         assert torch.equal(o, want) and torch.equal(o2, want2)
+
+
+def test_calls_back_to_back_equal_calls_one_by_one():
+    """Each call may start while the one before it ends: what it reads (the norm's codes, a
+    product's rows, weights quantised just before) and the buffers it writes over are those of
+    calls before it, over and over, on one stream and in a graph."""
+    g = _gen(77)
+    M, H, N = 300, 1024, 640
+    x = torch.randn((M, H), generator=g, device="cuda").to(BF16)
+    nw = torch.rand((H,), generator=g, device="cuda").to(BF16)
+    ws = [(torch.randn(s, generator=g, device="cuda") / s[0] ** 0.5).to(BF16) for s in ((H, N), (N, H))]
+    buf = dict(res=torch.empty_like(x), y8=torch.empty((M, H), dtype=torch.float8_e4m3fn, device="cuda"),
+               y8_scale=torch.empty((M, H // 128), dtype=E8, device="cuda"))
+    qw = [binding.quantize_weight_fp8(w) for w in ws]
+    h = torch.empty((M, N), dtype=BF16, device="cuda")
+    hq, hs = binding.quantize_rows_fp8(h.zero_())
+    o = torch.empty((M, H), dtype=BF16, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty((H,), dtype=F32, device="cuda")
+    inv = torch.empty((M,), dtype=F32, device="cuda")
+    back = torch.empty(binding.add_rmsnorm_backward_workspace_bytes(M, H), dtype=torch.uint8, device="cuda")
+
+    def run(steps, sync):
+        done = torch.cuda.synchronize if sync else lambda: None
+        cur, few = x, M
+        for i in range(steps):
+            few = (M, 17, 130)[i % 3]  # the kernels for long and short segments in turn
+            r = binding.add_rmsnorm(x, nw, cur, y=False, fp8=True, inv_rms=True, out=dict(buf, inv_rms=inv)); done()
+            binding.quantize_weight_fp8(ws[0], *qw[0]); done()
+            binding.linear_fp8(r["y8"][:few], r["y8_scale"][:few], *qw[0], out=h[:few]); done()
+            binding.quantize_rows_fp8(h, hq, hs); done()
+            binding.linear_fp8(hq, hs, *qw[1], out=o); done()
+            binding.add_rmsnorm_backward(o, r["res"], nw, inv, grads=dict(dx=dx, dweight=dw), ws=back); done()
+            cur = dx
+        return [t.clone() for t in (buf["res"], h, o, dx, dw)]
+
+    h.zero_()
+    want = run(30, True)
+    for _ in range(3):
+        h.zero_()
+        for a, b in zip(want, run(30, False)):
+            assert torch.equal(a, b)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(3, False)
+        graph = torch.cuda.CUDAGraph()
+        h.zero_()
+        with torch.cuda.graph(graph, stream=s):
+            got = run(30, False)
+        for t in (h, o, dx):
+            t.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
