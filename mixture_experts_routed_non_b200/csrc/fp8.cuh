@@ -53,7 +53,7 @@ inline bool fp8_sizes_ok(int64_t P, int32_t E, int32_t K, int32_t N) {
     return units < INT32_MAX / 2 && (int64_t)K * N < ((int64_t)1 << 39);
 }
 cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);       // picks the kernel
-// few rows, e8m0; chunk: 32 or 64 rows
+// few rows, e8m0; chunk: 32 or 64 rows, or 128 of one segment
 cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int chunk, int num_sms, cudaStream_t s);
 cudaError_t launch_fp8_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);     // 256-row tiles, any scales
 cudaError_t launch_fp8_mx_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);  // 256-row tiles, e8m0

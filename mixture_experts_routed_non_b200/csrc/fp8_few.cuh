@@ -270,16 +270,56 @@ inline bool make_few_maps(Fp8GemmArgs &a, int cn, bool rows) {
     return !rows || make_map_u8(&a.tmap_a, a.a, 2, ad, as, ab);
 }
 
+inline cudaLaunchAttribute few_cluster(int S) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)S;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    return at;
+}
+// A few-row kernel's shared memory, and how many clusters of 2, 4 and 8 CTAs run at
+// once (a byte each): one to an SM, but a cluster's SMs have to be neighbours.
+inline cudaError_t few_setup(void (*kernel)(Fp8GemmArgs), int threads, size_t smem, int *clusters) {
+    return launch_setup_once((const void *)kernel, clusters, [&](int, int *v) -> cudaError_t {
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        *v = 0;
+        for (int i = 0, S = 2; err == cudaSuccess && S <= kFMaxSplit; ++i, S *= 2) {
+            cudaLaunchAttribute at = few_cluster(S);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(S);
+            cfg.blockDim = dim3(threads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            int n = 0;
+            err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            *v |= (n < 255 ? n : 255) << (8 * i);
+        }
+        return err;
+    });
+}
+
+// CTAs to a unit: K is split while all clusters still run at once and each CTA keeps a
+// group of four blocks.  A cluster too many waits for a whole unit: 128 x 7168 x 512 in 16
+// clusters of eight, of which 15 run at once, 19.0 us, in clusters of four 10.3; 96 x
+// 2048 x 1536 in 36 clusters of four, of which 33, 14.1 us, of two 8.6.
+inline int few_split(int64_t units, int nk, int fit) {
+    int S = 1;
+    for (int i = 0; S < kFMaxSplit && units <= ((fit >> (8 * i)) & 255) && nk >= 8 * S; ++i) S *= 2;
+    return S;
+}
+
 // Launches a few-row kernel with chunks of cn rows on as many CTAs as there can be
 // units, split over K where there are few.
 inline cudaError_t launch_few(void (*kernel)(Fp8GemmArgs), Fp8GemmArgs &a, int cn, int n_tiles, int threads, size_t smem,
                               int num_sms, cudaStream_t s) {
+    int fit = 0;
+    const cudaError_t err = few_setup(kernel, threads, smem, &fit);
+    if (err != cudaSuccess) return err;
     // one segment: its chunks; else no more than P / cn and one begun per expert
     const int64_t chunks = a.expert_off ? a.P / cn + (a.E < a.P ? a.E : a.P) : (a.P + cn - 1) / cn;
     const int64_t units = chunks * n_tiles;
-    // split K while the clusters still fit one CTA to an SM and keep a group of four blocks each
-    int S = 1;
-    while (S < kFMaxSplit && units * S * 2 <= num_sms && a.nk >= 8 * S) S *= 2;
+    const int S = few_split(units, a.nk, fit);
     a.split = S;
     int64_t clusters = num_sms / S;
     if (clusters > units) clusters = units;
@@ -295,10 +335,7 @@ inline cudaError_t launch_few(void (*kernel)(Fp8GemmArgs), Fp8GemmArgs &a, int c
         attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
     if (S > 1) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = (unsigned)S;
-        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
-        ++cfg.numAttrs;
+        attr[cfg.numAttrs++] = few_cluster(S);
     }
     return cudaLaunchKernelEx(&cfg, kernel, (Fp8GemmArgs)a);
 }

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
 #pragma unroll
                 for (int t = 0; t < C::kAcc; ++t) tmem_st_x4(sf + 4 * t, cw[t], cw[t], cw[t], cw[t]);
                 // (columns past the chunk's CN rows are not read)
-                tmem_st_x4(sf + 4 * C::kAcc, ca[0], ca[kR - 1], ca[kR - 1], ca[kR - 1]);
+                tmem_st_x4(sf + 4 * C::kAcc, ca[0], ca[kR > 1 ? 1 : 0], ca[kR > 2 ? 2 : 0], ca[kR > 3 ? 3 : 0]);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -391,12 +391,6 @@ template <int CN, int kMode, bool kGather>
 cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     using C = FCfg<CN, kMode>;
     auto *kernel = fp8_few_kernel<CN, kMode, kGather>;
-    int unused = 0;
-    cudaError_t err = launch_setup_once((const void *)kernel, &unused, [&](int, int *v) -> cudaError_t {
-        *v = 1;
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-    });
-    if (err != cudaSuccess) return err;
     if (!make_few_maps(a, CN, !kGather)) return cudaErrorInvalidValue;
     return launch_few(kernel, a, CN, kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM, kGather ? 448 : 384, C::kSmem,
                       num_sms, s);
@@ -406,6 +400,8 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int chunk, int num_sms, cudaStream_t s) {
     const bool c32 = chunk == 32;
+    if (chunk == 128)  // one segment only
+        return mode == kFp8Bf16 && !a.gather ? launch_one<128, kFp8Bf16, false>(a, num_sms, s) : cudaErrorInvalidValue;
     if (mode == kFp8SwiGlu)
         return c32 ? launch_one<32, kFp8SwiGlu, true>(a, num_sms, s) : launch_one<64, kFp8SwiGlu, true>(a, num_sms, s);
     if (mode == kFp8Y16)

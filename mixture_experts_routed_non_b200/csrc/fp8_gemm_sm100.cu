@@ -312,12 +312,6 @@ template <int kMode, bool kGather>
 cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     using C = QCfg<kMode>;
     auto *kernel = fp8_few_any_kernel<kMode, kGather>;
-    int unused = 0;
-    cudaError_t err = launch_setup_once((const void *)kernel, &unused, [&](int, int *v) -> cudaError_t {
-        *v = 1;
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-    });
-    if (err != cudaSuccess) return err;
     if (!make_few_maps(a, CN, !kGather)) return cudaErrorInvalidValue;
     return launch_few(kernel, a, CN, kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM, kGather ? 320 : 256,
                       C::kSmem, num_sms, s);
@@ -330,31 +324,66 @@ cudaError_t launch_any_few(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s
     return a.gather ? launch_one<kFp8Bf16, true>(a, num_sms, s) : launch_one<kFp8Bf16, false>(a, num_sms, s);
 }
 
-}  // namespace
+// How many clusters run at once (few_setup): the same for every few-row kernel, one CTA to an SM.
+cudaError_t any_few_setup(int *fit) { return few_setup(fp8_few_any_kernel<kFp8Bf16, false>, 256, QCfg<kFp8Bf16>::kSmem, fit); }
 
 // Which kernel.  Four: few rows or 256-row tiles on CTA pairs, scales by the tensor
 // cores (both e8m0) or in the epilogue (any fp32).  Times below in us, in a graph.
-//   One segment: the few-row kernels while their units (chunk x 128 weight rows) fit
-//   one to an SM, chunks of 32 rows up to 32 rows or 2048 of K, else of 64 (fewer
-//   chunks re-read the weights less, but a chunk of 64 costs a longer epilogue):
-//     K 7168, N 4096   rows      16    64   128   256   512
-//       chunks of 32            10.9  20.2  20.6  36.2  67.2
-//       chunks of 64            11.3  15.9  22.2  22.6  39.5
-//       pairs                   22.1  22.3  22.9  23.2  23.5
-//     K 2048, N 1536: rows 256: 9.5, 10.2, 11.7; 512: 14.2, 10.8, 11.8; 1024: 19.2, 15.7, 11.9
-//     scales in fp32, K 7168, N 4096: rows 128: 27 (chunks of 32), 43 (pairs); 256: 50, 44
-//   Segments: only their average is known here.  e8m0, 128 experts, K 768, N 2048, average
-//   rows 8 / 16 / 32 / 64 / 128: chunks of 32 37, 38, 47, 75, 130; chunks of 64 36, 37,
-//   39, 63, 95; pairs 52, 54, 55, 57, 62; skewed to an average of 4: 33, 34, 45.
+//
+// One segment: the kernel and chunk of least time by a straight line that fits what was
+// measured within a tenth: a start, and per wave of units (or tiles) a time per block of
+// 128 K; a split of K over 2 or 4 CTAs costs 2.2 more, over 8 3.5.
+//   e8m0                       start  block   fp32 scales   start  block
+//     few rows, chunks of 32     4.6  0.275                   4.0  0.385
+//                         64     5.7  0.295
+//                        128     8.0  0.325
+//     pairs                      6.3  0.291                   5.7  0.49
+//   (pairs with e8m0: 5 % above the fit, 6.0 and 0.277.  Where others come as near, rows whose
+//   pitch is no multiple of 32 bytes decide: 600 x 2992 x 1000 12.5 in chunks of 64, 15.0 in pairs.)
+//   Measured, K 7168, N 4096    rows   16    48    96   128   256   384   512
+//     chunks of 32                   10.0  14.2  20.0  20.0  35.6  51.2  66.3
+//     chunks of 64                         12.4  16.1  16.2  22.1  38.6  38.8
+//     chunks of 128                        13.2  14.4  15.5  19.6  25.8  26.0
+//     pairs                                21.4  21.8  22.1  22.3  22.7  23.7
+//   K 2048, N 1536: rows 128: 8.6, 8.9, 10.3, 10.6; 384: 9.1, 10.2, 12.2, 10.7; 768: 14.1,
+//     10.5, 13.1, 10.9; 1024: 18.7, 15.4, 12.9, 11.0
+//   fp32 scales, K 7168, N 4096: rows 128: 25.6 (chunks of 32), 33.3 (pairs); 256: 47.7, 34.1
+// Segments: only their average is known here.  e8m0, 128 experts, K 768, N 2048, average
+// rows 16 / 32 / 48 / 64 / 96: chunks of 32 37, 47, 62, 76, 105; chunks of 64 37, 38, 41,
+// 60, 81; pairs 50, 52, 53, 54, 56.  (Chunks of 128 only help near 64, by 48 to 54, and not
+// where experts are unequal: 63 to 58.)
+struct Kernels {
+    int chunk;  // rows; 0: pairs
+    float start, block;
+};
+constexpr Kernels kE8m0Times[] = {{32, 4.6f, 0.275f}, {64, 5.7f, 0.295f}, {128, 8.0f, 0.325f}, {0, 6.3f, 0.291f}};
+constexpr Kernels kF32Times[] = {{32, 4.0f, 0.385f}, {0, 5.7f, 0.49f}};
+
+float expected_us(const Kernels &k, const Fp8GemmArgs &a, int num_sms, int fit) {
+    const int64_t rows = k.chunk ? k.chunk : kPM, cols = k.chunk ? kFM : kPN;
+    const int64_t units = (a.P + rows - 1) / rows * ((a.N + cols - 1) / cols);
+    const int S = k.chunk ? few_split(units, a.nk, fit) : 1, at_once = k.chunk ? num_sms / S : num_sms / 2;
+    const float waves = (float)((units + at_once - 1) / at_once);
+    return k.start + k.block * waves * (float)((a.nk + S - 1) / S) + (S == 1 ? 0.f : S < 8 ? 2.2f : 3.5f);
+}
+
+}  // namespace
+
 cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     if (a.P == 0 || a.N == 0) return cudaSuccess;
     const bool e8m0 = !a.a_f32 && !a.w_f32;
     int chunk = 0;  // rows per chunk of the few-row kernels; 0: pairs
     if (!a.expert_off) {
-        const int64_t tiles = (a.N + 127) / 128;
-        const bool fit32 = (a.P + 31) / 32 * tiles <= num_sms, fit64 = (a.P + 63) / 64 * tiles <= num_sms;
-        if (!e8m0) chunk = fit32 ? 32 : 0;
-        else chunk = fit32 && (a.P <= 32 || a.nk <= 16) ? 32 : fit64 ? 64 : 0;
+        int fit = 0;
+        const cudaError_t err = any_few_setup(&fit);
+        if (err != cudaSuccess) return err;
+        float least = 0.f;
+        auto pick = [&](const Kernels &k) {
+            const float us = expected_us(k, a, num_sms, fit);
+            if (least == 0.f || us < least) least = us, chunk = k.chunk;
+        };
+        if (e8m0) for (const Kernels &k : kE8m0Times) pick(k);
+        else for (const Kernels &k : kF32Times) pick(k);
     } else {
         if (!e8m0) chunk = a.P <= 32ll * a.E ? 32 : 0;
         else chunk = a.P <= 16ll * a.E ? 32 : a.P <= 48ll * a.E ? 64 : 0;

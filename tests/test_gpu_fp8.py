@@ -450,6 +450,32 @@ def test_two_products_on_two_streams():
         assert torch.equal(o, want) and torch.equal(o2, want2)
 
 
+@pytest.mark.parametrize("M,K,N", [(100, 7168, 4096), (130, 7168, 4096), (255, 7008, 4088)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_linear_of_a_hundred_or_two_rows_on_a_large_matrix(M, K, N, bias):
+    g = _gen(M + N)
+    a, s = ref.make_rows(g, M, K, E8, "cuda")
+    w, t = ref.make_weight(g, 1, N, K, E8, "cuda")
+    b = torch.randn((N,), generator=g, device="cuda").to(BF16) if bias else None
+    out = torch.full((M + 3, N), 9.0, dtype=BF16, device="cuda")
+    binding.linear_fp8(a, s, w[0], t[0], b, out=out[:M])
+    y, tol = ref.product(ref.values(a, s), ref.weight_values(w[0], t[0]), b)
+    ref.check(out[:M], y, tol)
+    assert bool((out[M:] == 9).all())
+
+
+@pytest.mark.parametrize("M,K,N", [(96, 2048, 1536), (128, 7168, 512), (256, 7168, 512), (33, 1024, 1200)])
+@pytest.mark.parametrize("scale", [E8, F32])
+def test_linear_split_over_clusters(M, K, N, scale):
+    g = _gen(M + K)
+    a, s = ref.make_rows(g, M, K, scale, "cuda")
+    w, t = ref.make_weight(g, 1, N, K, scale, "cuda")
+    y, tol = ref.product(ref.values(a, s), ref.weight_values(w[0], t[0]), None)
+    first = binding.linear_fp8(a, s, w[0], t[0])
+    ref.check(first, y, tol)
+    assert torch.equal(first, binding.linear_fp8(a, s, w[0], t[0]))
+
+
 def test_calls_back_to_back_equal_calls_one_by_one():
     """Each call may start while the one before it ends: what it reads (the norm's codes, a
     product's rows, weights quantised just before) and the buffers it writes over are those of
