@@ -497,7 +497,8 @@ MOE_API int moe_ep_combine(const moe_ep_sources_t *src, const int32_t *send_idx,
  * ([M,K]: scales [M, ceil(K/128)]), per 128 x 128 values of a weight
  * ([E,N,K]: scales [E, ceil(N/128), ceil(K/128)]).  The value is code * scale.
  * A scale is a power of two held as e8m0 (MOE_SCALE_E8M0: byte b stands for
- * 2^(b-127), 255 for NaN) or any fp32 (MOE_SCALE_F32).
+ * 2^(b-127), 255 for NaN) or any fp32 (MOE_SCALE_F32).  e8m0 scales may start
+ * at any byte and are read in the aligned 32-bit words that they lie in.
  *
  * The quantisers here (the norm's 8-bit output, moe_fp8_quantize_*) write
  * e8m0: the smallest power of two s with amax <= 448 s, amax being the block's

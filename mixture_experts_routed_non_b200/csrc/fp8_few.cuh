@@ -135,12 +135,28 @@ __device__ __forceinline__ void partials_read(uint32_t rempty_bar, int S, int la
     }
 }
 
+// Which of a unit's rows are gathered from outside `a`.  The sources are loaded before the
+// wait for the accumulator, which hides it, and looked at behind it.
+template <int CN>
+struct FGone {
+    int src[CN / 32];
+    uint32_t bits[CN / 32];
+    __device__ __forceinline__ void load(const Fp8GemmArgs &a, const FUnit &q, int lane) {
+#pragma unroll
+        for (int i = 0; i < CN / 32; ++i) src[i] = 32 * i + lane < q.nv ? __ldg(a.gather + q.m0 + 32 * i + lane) : 0;
+    }
+    __device__ __forceinline__ void look(const Fp8GemmArgs &a) {
+#pragma unroll
+        for (int i = 0; i < CN / 32; ++i) bits[i] = __ballot_sync(0xffffffffu, src[i] < 0 || src[i] >= a.rows);
+    }
+};
+
 // The unit's output for the tokens of this CTA, by 128 threads (tid).  red (its
 // shared-memory address; red_ptr the same): [tile][token][weight row] fp32 in each of
 // the S CTAs.
 template <int CN, int kMode, bool kGather>
 __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q, int rank, int S, int tid, bool concat,
-                                           uint32_t red, const uint8_t *red_ptr, bool ok) {
+                                           uint32_t red, const uint8_t *red_ptr, const FGone<CN> &gone, bool ok) {
     constexpr int kAcc = kMode == kFp8SwiGlu ? 2 : 1;
     // Tokens rank, rank + S, ...: eight at a time, 16 threads each, eight neighbouring
     // columns per thread.
@@ -174,11 +190,7 @@ __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q,
             for (int i = 0; i < 8; ++i) v[i] += __bfloat162float(br[i]);
         };
         const size_t p = (size_t)q.m0 + jj;
-        bool outside = false;  // a gathered row outside `a` counts as zeros
-        if (kGather) {
-            const int src = __ldg(a.gather + p);
-            outside = src < 0 || src >= a.rows;
-        }
+        const bool outside = kGather && (gone.bits[jj >> 5] >> (jj & 31) & 1);  // counts as zeros
         auto keep = [&](float (&v)[8]) {
             if (kGather && outside)
 #pragma unroll

@@ -256,7 +256,6 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         constexpr int kR = CN / 32;  // rows of `a` per lane
         const int nb = (a.N + 127) / 128, nk = a.nk;
         const uint8_t *as = static_cast<const uint8_t *>(a.a_scale), *ws = static_cast<const uint8_t *>(a.w_scale);
-        const int ha = e8m0_rows(as, nk | kb0), hw = e8m0_rows(ws, nk | kb0);
         const uint32_t sf0 = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + C::kScale0;
         int slot = 0;
         uint32_t phase = 0;
@@ -265,7 +264,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         FUnit q = {};
         int srow[kR], nrow[kR];
         size_t wi[C::kAcc];
-        uint32_t ra[kR][2], rw[C::kAcc][2];
+        uint32_t ra[kR][2], rw[C::kAcc][2], shifts;
         auto load_rows = [&](int u) {
             if (u < units) q = list.at(u);
 #pragma unroll
@@ -282,14 +281,12 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         };
         auto load_group = [&](int kb) {
             const int last = kb1 - 1 - kb;
+            shifts = 0;
 #pragma unroll
-            for (int i = 0; i < kR; ++i) {
-                ra[i][0] = 0x7F7F7F7Fu;
-                ra[i][1] = 0;
-                if (srow[i] >= 0) load_e8m0_x4(as, (size_t)srow[i] * nk + kb, last, ha, ra[i][0], ra[i][1]);
-            }
+            for (int i = 0; i < kR; ++i)  // (-1: some row's scales, for accumulator columns that are dropped)
+                load_e8m0_x4(as, (size_t)max(srow[i], 0) * nk + kb, last, ra[i][0], ra[i][1], shifts);
 #pragma unroll
-            for (int t = 0; t < C::kAcc; ++t) load_e8m0_x4(ws, wi[t] + kb, last, hw, rw[t][0], rw[t][1]);
+            for (int t = 0; t < C::kAcc; ++t) load_e8m0_x4(ws, wi[t] + kb, last, rw[t][0], rw[t][1], shifts);
         };
         bool ok = true;
         if (u0 < units) {
@@ -302,9 +299,9 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
             for (int kb = kb0; ok && kb < kb1; kb += 4) {
                 uint32_t ca[kR], cw[C::kAcc];
 #pragma unroll
-                for (int i = 0; i < kR; ++i) ca[i] = ra[i][0] | ra[i][1] << 16;
+                for (int i = 0; i < kR; ++i) ca[i] = e8m0_word(ra[i][0], ra[i][1], shifts, kR + C::kAcc - 1 - i);
 #pragma unroll
-                for (int t = 0; t < C::kAcc; ++t) cw[t] = rw[t][0] | rw[t][1] << 16;
+                for (int t = 0; t < C::kAcc; ++t) cw[t] = e8m0_word(rw[t][0], rw[t][1], shifts, C::kAcc - 1 - t);
                 if (kb + 4 < kb1) {
                     load_group(kb + 4);
                 } else if (u + du < units) {
@@ -339,10 +336,13 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         for (int u = u0; u < units; u += du, ++it) {
             const FUnit q = list.at(u);
             const uint32_t b = it & 1u;
+            FGone<CN> gone;
+            if (kGather) gone.load(a, q, lane);
             mbar_wait_bounded(tfull_bar(b), (it >> 1) & 1u, abort);
             // the partial sums of the unit before have been read, here and by the peers
             mbar_wait_bounded(rempty_bar, (it & 1u) ^ 1u, abort);
             __syncwarp();
+            if (kGather) gone.look(a);
             tc_fence_after();
 #pragma unroll
             for (int t = 0; t < C::kAcc; ++t)
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
             if (lane == 0) mbar_arrive(tempty_bar(b));
             partials_ready(rfull_bar, it & 1u, S, lane, abort);
             const bool ok = *abort == 0;
-            few_output<CN, kMode, kGather>(a, q, rank, S, tid, concat, red, base_ptr + C::kRedOff, ok);
+            few_output<CN, kMode, kGather>(a, q, rank, S, tid, concat, red, base_ptr + C::kRedOff, gone, ok);
             partials_read(rempty_bar, S, lane);
         }
     } else if (kGather && warp >= 12) {

@@ -283,10 +283,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         // and a tile's row numbers a tile ahead: a tile's first scales would otherwise be two
         // dependent loads (thousands of clocks under load) behind the operands.
         PTile t;
-        int srow[4], nrow[4];  // rows of `a`; -1: past the segment or outside `a` (zeros, or never stored)
+        int srow[4], nrow[4];  // rows of `a`; -1: past the segment or outside `a` (never stored, or stored as zeros)
         size_t wi[2];
-        uint32_t ra[4][2], rw[2][2];
-        const int ha = e8m0_rows(as, nk), hw = e8m0_rows(ws, nk);
+        uint32_t ra[4][2], rw[2][2], shifts;
         auto load_rows = [&](int u) {
             if (u < tiles) t = list.at(u);
 #pragma unroll
@@ -304,14 +303,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         };
         auto load_group = [&](int kb) {
             const int last = nk - 1 - kb;
+            shifts = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ra[i][0] = 0x7F7F7F7Fu;
-                ra[i][1] = 0;
-                if (srow[i] >= 0) load_e8m0_x4(as, (size_t)srow[i] * nk + kb, last, ha, ra[i][0], ra[i][1]);
-            }
+            for (int i = 0; i < 4; ++i)  // (-1: some row's scales, for accumulator rows that are dropped)
+                load_e8m0_x4(as, (size_t)max(srow[i], 0) * nk + kb, last, ra[i][0], ra[i][1], shifts);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) load_e8m0_x4(ws, wi[h] + kb, last, hw, rw[h][0], rw[h][1]);
+            for (int h = 0; h < 2; ++h) load_e8m0_x4(ws, wi[h] + kb, last, rw[h][0], rw[h][1], shifts);
         };
         bool ok = true;
         if (t0 < tiles) {
@@ -324,9 +321,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             for (int kb = 0; ok && kb < nk; kb += 4) {
                 uint32_t ca[4], cw[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ca[i] = ra[i][0] | ra[i][1] << 16;
+                for (int i = 0; i < 4; ++i) ca[i] = e8m0_word(ra[i][0], ra[i][1], shifts, 5 - i);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) cw[h] = rw[h][0] | rw[h][1] << 16;
+                for (int h = 0; h < 2; ++h) cw[h] = e8m0_word(rw[h][0], rw[h][1], shifts, 1 - h);
                 if (kb + 4 < nk) {
                     load_group(kb + 4);
                 } else if (u + dt < tiles) {

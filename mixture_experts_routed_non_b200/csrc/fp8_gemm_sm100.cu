@@ -225,6 +225,8 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
         // barriers and store nothing
         for (int u = u0; u < units; u += du, ++uc) {
             const FUnit q = list.at(u);
+            FGone<CN> gone;
+            if (kGather) gone.load(a, q, lane);
             float acc[C::kAcc][CN];
 #pragma unroll
             for (int t = 0; t < C::kAcc; ++t)
@@ -277,12 +279,14 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
             // the partial sums of the unit before have been read, here and by the peers
             mbar_wait_bounded(rempty_bar, (uc & 1u) ^ 1u, abort);
             __syncwarp();
+            if (kGather) gone.look(a);
 #pragma unroll
             for (int t = 0; t < C::kAcc; ++t)
 #pragma unroll
                 for (int j = 0; j < CN; ++j) red_s[(t * CN + j) * kFM + 32 * q4 + lane] = acc[t][j];
             partials_ready(rfull_bar, uc & 1u, S, lane, abort);
-            few_output<CN, kMode, kGather>(a, q, rank, S, tid, concat, red, base_ptr + C::kRedOff, *abort == 0);
+            few_output<CN, kMode, kGather>(a, q, rank, S, tid, concat, red, base_ptr + C::kRedOff, gone,
+                                           *abort == 0);
             partials_read(rempty_bar, S, lane);
         }
     } else if (kGather && warp >= 8) {

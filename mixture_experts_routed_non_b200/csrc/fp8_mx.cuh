@@ -23,26 +23,24 @@ __device__ __forceinline__ void tmem_st_x4(uint32_t taddr, uint32_t r0, uint32_t
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The e8m0 bytes i .. i + 3 of a row of scales, as two registers that make up one
-// word by r0 | r1 << 16 -- later: nothing here waits for the loads, except where a
-// row starts at an odd byte.  how: 0 rows of whole words, 1 of half-words, 2 bytes.
-__device__ __forceinline__ void load_e8m0_x4(const uint8_t *p, size_t i, int last, int how, uint32_t &r0, uint32_t &r1) {
-    const uint8_t *q = p + i;
-    r1 = 0;
-    if (how == 0) {
-        r0 = __ldg(reinterpret_cast<const uint32_t *>(q));
-    } else if (how == 1) {
-        r0 = __ldg(reinterpret_cast<const uint16_t *>(q));
-        if (last >= 2) r1 = __ldg(reinterpret_cast<const uint16_t *>(q + 2));
-    } else {  // behind `last` the last byte again: never used
-        const uint32_t b0 = __ldg(q), b1 = __ldg(q + min(1, last)), b2 = __ldg(q + min(2, last)),
-                       b3 = __ldg(q + min(3, last));
-        r0 = b0 | b1 << 8 | b2 << 16 | b3 << 24;
-    }
+// The e8m0 bytes i .. i + 3 of a row of scales, up to `last` of them behind the first, in
+// two registers: the aligned words they lie in (the second only where it holds one of
+// them), and the shift that brings the first byte to the bottom in the low five bits of the
+// next field of `shifts`.  e8m0_word joins them -- later: nothing here waits for the loads,
+// so that a group's loads are in flight together whatever byte its rows start at (byte
+// loads joined on the spot cost 3000 clocks a tile where a row has three scales).
+__device__ __forceinline__ void load_e8m0_x4(const uint8_t *p, size_t i, int last, uint32_t &r0, uint32_t &r1,
+                                             uint32_t &shifts) {
+    const uintptr_t q = reinterpret_cast<uintptr_t>(p + i);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(q & ~(uintptr_t)3);
+    const uint32_t skip = (uint32_t)q & 3u;
+    r0 = __ldg(w);
+    r1 = skip + (uint32_t)min(last, 3) > 3u ? __ldg(w + 1) : 0u;
+    shifts = shifts << 5 | skip << 3;
 }
-__device__ __forceinline__ int e8m0_rows(const uint8_t *p, int nk) {
-    const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(p) | (uint32_t)nk;
-    return (a & 3) == 0 ? 0 : (a & 1) == 0 ? 1 : 2;
+// field: 0 for the last one loaded, 1 for the one before, ...
+__device__ __forceinline__ uint32_t e8m0_word(uint32_t r0, uint32_t r1, uint32_t shifts, int field) {
+    return __funnelshift_r(r0, r1, shifts >> (5 * field));  // (by the low five bits)
 }
 
 #endif  // __CUDACC__
