@@ -25,6 +25,7 @@ constexpr int kFMaxSplit = 8;
 
 constexpr uint32_t kFTileW = kFM * kPK;   // 16 KB
 constexpr int kFGather = 64;              // gather threads
+constexpr int kFListed = 64;              // a CTA's first units, looked up once
 
 // Cluster-scope release and acquire: shared-memory data handed to another CTA.
 __device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_addr) {
@@ -45,13 +46,44 @@ struct FUnit {
 };
 
 // Units: experts in order, inside one its weight tiles, inside a tile its chunks.
-// off_s and pre_s (chunks below each expert) are shared-memory tables of E + 1.
-template <int CN, int kMode>
+// off_s and pre_s (chunks below each expert) are shared-memory tables of E + 1, first one
+// of the CTA's first kFListed units (as in PTiles).  kOne: one segment, no tables.
+template <int CN, int kMode, bool kOne>
 struct FUnits {
     const int *off_s, *pre_s;
-    int E, N, n_tiles;
+    int4 *first;
+    int listed;
+    int E, N, n_tiles, P;
     bool concat;
-    __device__ __forceinline__ FUnit at(int u) const {
+    __device__ __forceinline__ void fill(int units, int u0, int du) {
+        if (kOne) return;
+        const int i = (int)threadIdx.x;
+        listed = units > 2 * du ? kFListed : 0;
+        if (listed == 0) return;
+        if (i < kFListed && u0 + i * du < units) {
+            const FUnit q = find(u0 + i * du);
+            first[i] = make_int4(q.e, q.nt, q.m0, q.nv);
+        }
+        __syncthreads();
+    }
+    // unit u, the CTA's i-th
+    __device__ __forceinline__ FUnit at(int u, int i) const {
+        if (kOne || i >= listed) return find(u);
+        const int4 v = first[i];
+        FUnit q;
+        q.e = v.x, q.nt = v.y, q.m0 = v.z, q.nv = v.w;
+        return q;
+    }
+    __device__ __forceinline__ FUnit find(int u) const {
+        if (kOne) {
+            const int ch = (P + CN - 1) / CN;
+            FUnit q;
+            q.e = 0;
+            q.nt = ch == 1 ? u : u / ch;
+            q.m0 = (u - q.nt * ch) * CN;
+            q.nv = min(CN, P - q.m0);
+            return q;
+        }
         int lo = 0, hi = E - 1;  // the expert whose units hold u (empty experts hold none)
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -79,15 +111,15 @@ struct FUnits {
 // piece (g & 7) of rows (g >> 3) + 8 i to row * 128 + ((piece ^ (row & 7)) << 4) (the
 // 128-byte swizzle) of each stage's rows; sources as in fp8_pair.cuh.
 template <int CN, int kMode, int kStages, uint32_t kStage, uint32_t kStageW, typename Empty, typename Gfull>
-__device__ __forceinline__ void gather_chunk_rows(const Fp8GemmArgs &a, const FUnits<CN, kMode> &list, int units, int u0,
+__device__ __forceinline__ void gather_chunk_rows(const Fp8GemmArgs &a, const FUnits<CN, kMode, false> &list, int units, int u0,
                                                   int du, int kb0, int kb1, int g, uint32_t base, Empty empty_bar,
                                                   Gfull gfull_bar, volatile uint32_t *abort) {
     const int piece = g & 7, r0 = g >> 3;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u = u0; ok && u < units; u += du) {
-        const FUnit q = list.at(u);
+    for (int u = u0, n = 0; ok && u < units; u += du, ++n) {
+        const FUnit q = list.at(u, n);
         int row[CN / 8];  // -1: not copied
 #pragma unroll
         for (int i = 0; i < CN / 8; ++i)

@@ -41,7 +41,8 @@ struct FCfg {
     static constexpr size_t kRedOff = (size_t)kStages * kStage;
     static constexpr size_t kBarOff = kRedOff + kRed;
     static constexpr size_t kMiscOff = kBarOff + 8 * kBars + 8;
-    static constexpr size_t kTableOff = (kMiscOff + 16 + 15) / 16 * 16;
+    static constexpr size_t kFirstOff = (kMiscOff + 16 + 15) / 16 * 16;
+    static constexpr size_t kTableOff = kFirstOff + kFListed * 16;
     static constexpr size_t kSmem = 1024 + kTableOff + 2 * (kMaxExperts + 1) * 4;
     static_assert(kSmem <= 232448, "shared memory of one CTA (227 KB)");
 };
@@ -56,7 +57,7 @@ __device__ __forceinline__ void umma_mx(uint32_t d_tmem, uint64_t a_desc, uint64
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
         : "memory");
 }
-template <int CN, int kMode, bool kGather>
+template <int CN, int kMode, bool kGather, bool kOne>
 __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const __grid_constant__ Fp8GemmArgs a) {
     using C = FCfg<CN, kMode>;
     constexpr int kThreads = kGather ? 448 : 384;
@@ -109,9 +110,11 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
     }
     if (kMode != kFp8Y16) pdl_wait();
     pdl_launch_dependents();
-    load_offsets(a, off_s, kThreads);
-    __syncthreads();
-    if (warp == 0) {
+    if (!kOne) {
+        load_offsets(a, off_s, kThreads);
+        __syncthreads();
+    }
+    if (!kOne && warp == 0) {
         prefix_pieces(off_s, pre_s, E, a.P, CN, lane);
         // nothing to do when the metadata found more pairs than the arrays hold
         if (lane == 0) misc[3] = a.hdr && load_now(&a.hdr->abort) ? 0u : (uint32_t)pre_s[E];
@@ -129,11 +132,13 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
     volatile uint32_t *abort = &misc[1];
     const bool concat = kMode == kFp8SwiGlu && a.layout == MOE_LAYOUT_CONCATENATED;
     const int n_tiles = kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM;
-    const int units = (int)misc[3] * n_tiles;  // below 2^31 (fp8_sizes_ok)
+    const int units = (kOne ? ((int)a.P + CN - 1) / CN : (int)misc[3]) * n_tiles;  // below 2^31 (fp8_sizes_ok)
     const int u0 = S > 1 ? (int)blockIdx.x / S : (int)blockIdx.x, du = S > 1 ? (int)gridDim.x / S : (int)gridDim.x;
     // this CTA's share of the scale blocks along K
     const int kb0 = (int)((long long)a.nk * rank / S), kb1 = (int)((long long)a.nk * (rank + 1) / S);
-    const FUnits<CN, kMode> list{off_s, pre_s, E, a.N, n_tiles, concat};
+    FUnits<CN, kMode, kOne> list{off_s,   pre_s,      reinterpret_cast<int4 *>(base_ptr + C::kFirstOff), 0, E, a.N,
+                                 n_tiles, (int)a.P, concat};
+    list.fill(units, u0, du);
 
     if (warp == 0) {
         // -------------------------------------------------- producer: weights
@@ -141,8 +146,8 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int u = u0; ok && u < units; u += du) {
-            const FUnit q = list.at(u);
+        for (int u = u0, n = 0; ok && u < units; u += du, ++n) {
+            const FUnit q = list.at(u, n);
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                 if (!ok) break;
@@ -167,8 +172,8 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int u = u0; ok && u < units; u += du) {
-            const FUnit q = list.at(u);
+        for (int u = u0, n = 0; ok && u < units; u += du, ++n) {
+            const FUnit q = list.at(u, n);
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                 if (!ok) break;
@@ -265,8 +270,9 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         int srow[kR], nrow[kR];
         size_t wi[C::kAcc];
         uint32_t ra[kR][2], rw[C::kAcc][2], shifts;
+        int listed = 0;  // calls so far: the CTA's unit they are at
         auto load_rows = [&](int u) {
-            if (u < units) q = list.at(u);
+            if (u < units) q = list.at(u, listed++);
 #pragma unroll
             for (int i = 0; i < kR; ++i) {
                 const int j = 32 * i + lane;
@@ -333,8 +339,8 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         const uint32_t red = base + (uint32_t)C::kRedOff;
         float *red_s = reinterpret_cast<float *>(base_ptr + C::kRedOff);
         uint32_t it = 0;
-        for (int u = u0; u < units; u += du, ++it) {
-            const FUnit q = list.at(u);
+        for (int u = u0, n = 0; u < units; u += du, ++n, ++it) {
+            const FUnit q = list.at(u, n);
             const uint32_t b = it & 1u;
             FGone<CN> gone;
             if (kGather) gone.load(a, q, lane);
@@ -366,7 +372,8 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         }
     } else if (kGather && warp >= 12) {
         // -------------------------------------------------------- row gather
-        gather_chunk_rows<CN, kMode, kStages, C::kStage, C::kStageW>(a, list, units, u0, du, kb0, kb1,
+        if constexpr (kGather)
+            gather_chunk_rows<CN, kMode, kStages, C::kStage, C::kStageW>(a, list, units, u0, du, kb0, kb1,
                                                                      (int)threadIdx.x - 384, base, empty_bar,
                                                                      gfull_bar, abort);
     }
@@ -387,10 +394,10 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
     }
 }
 
-template <int CN, int kMode, bool kGather>
+template <int CN, int kMode, bool kGather, bool kOne>
 cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     using C = FCfg<CN, kMode>;
-    auto *kernel = fp8_few_kernel<CN, kMode, kGather>;
+    auto *kernel = fp8_few_kernel<CN, kMode, kGather, kOne>;
     if (!make_few_maps(a, CN, !kGather)) return cudaErrorInvalidValue;
     return launch_few(kernel, a, CN, kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM, kGather ? 448 : 384, C::kSmem,
                       num_sms, s);
@@ -401,14 +408,16 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
 cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int chunk, int num_sms, cudaStream_t s) {
     const bool c32 = chunk == 32;
     if (chunk == 128)  // one segment only
-        return mode == kFp8Bf16 && !a.gather ? launch_one<128, kFp8Bf16, false>(a, num_sms, s) : cudaErrorInvalidValue;
+        return mode == kFp8Bf16 && !a.expert_off ? launch_one<128, kFp8Bf16, false, true>(a, num_sms, s) : cudaErrorInvalidValue;
     if (mode == kFp8SwiGlu)
-        return c32 ? launch_one<32, kFp8SwiGlu, true>(a, num_sms, s) : launch_one<64, kFp8SwiGlu, true>(a, num_sms, s);
+        return c32 ? launch_one<32, kFp8SwiGlu, true, false>(a, num_sms, s) : launch_one<64, kFp8SwiGlu, true, false>(a, num_sms, s);
     if (mode == kFp8Y16)
-        return c32 ? launch_one<32, kFp8Y16, false>(a, num_sms, s) : launch_one<64, kFp8Y16, false>(a, num_sms, s);
+        return c32 ? launch_one<32, kFp8Y16, false, false>(a, num_sms, s) : launch_one<64, kFp8Y16, false, false>(a, num_sms, s);
     if (a.gather)
-        return c32 ? launch_one<32, kFp8Bf16, true>(a, num_sms, s) : launch_one<64, kFp8Bf16, true>(a, num_sms, s);
-    return c32 ? launch_one<32, kFp8Bf16, false>(a, num_sms, s) : launch_one<64, kFp8Bf16, false>(a, num_sms, s);
+        return c32 ? launch_one<32, kFp8Bf16, true, false>(a, num_sms, s) : launch_one<64, kFp8Bf16, true, false>(a, num_sms, s);
+    if (a.expert_off)
+        return c32 ? launch_one<32, kFp8Bf16, false, false>(a, num_sms, s) : launch_one<64, kFp8Bf16, false, false>(a, num_sms, s);
+    return c32 ? launch_one<32, kFp8Bf16, false, true>(a, num_sms, s) : launch_one<64, kFp8Bf16, false, true>(a, num_sms, s);
 }
 
 }  // namespace moe

@@ -47,7 +47,8 @@ struct PCfg {
     static constexpr size_t kMaxOff = kScaleOff + kPSlots * kPSlot * 4;  // SwiGlu: [4][128] row maxima
     static constexpr size_t kBarOff = kMaxOff + 4 * 128 * 4;
     static constexpr size_t kMiscOff = kBarOff + 8 * kBars;
-    static constexpr size_t kTableOff = kMiscOff + 16;
+    static constexpr size_t kFirstOff = (kMiscOff + 16 + 15) / 16 * 16;
+    static constexpr size_t kTableOff = kFirstOff + kPListed * 16;
     static constexpr size_t kSmem = 1024 + kTableOff + 2 * (kMaxExperts + 1) * 4;
     static_assert(kSmem <= 232448, "shared memory of one CTA (227 KB)");
 };
@@ -61,7 +62,7 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, u
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-template <int kMode, bool kGather>
+template <int kMode, bool kGather, bool kOne>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 1)
     fp8_pair_kernel(const __grid_constant__ Fp8GemmArgs a) {
     using C = PCfg<kMode>;
@@ -114,9 +115,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
     }
     if (kMode != kFp8Y16) pdl_wait();
     pdl_launch_dependents();
-    load_offsets(a, off_s, kPThreads);
-    __syncthreads();
-    if (warp == 0) {
+    if (!kOne) {
+        load_offsets(a, off_s, kPThreads);
+        __syncthreads();
+    }
+    if (!kOne && warp == 0) {
         prefix_pieces(off_s, pre_s, E, a.P, kPM, lane);
         // nothing to do when the metadata found more pairs than the arrays hold (the same word in
         // both CTAs of the pair)
@@ -134,8 +137,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
     volatile uint32_t *abort = &misc[1];
     const int nk = a.nk;
     const bool concat = kMode == kFp8SwiGlu && a.layout == MOE_LAYOUT_CONCATENATED;
-    const PTiles list{off_s, pre_s, E, a.N, (a.N + kPN - 1) / kPN, concat};
+    PTiles<kOne> list{off_s, pre_s, reinterpret_cast<int4 *>(base_ptr + C::kFirstOff), 0, E, a.N,
+                      (a.N + kPN - 1) / kPN, (int)a.P, concat};
     const int tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
+    list.fill(t0, dt);
 
     if (warp < 4) {
         regs_dec<p_other_regs(kGather)>();
@@ -146,8 +151,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_parity = 0;
             bool ok = true;
-            for (int u = t0; ok && u < tiles; u += dt) {
-                const PTile t = list.at(u);
+            for (int u = t0, i = 0; ok && u < tiles; u += dt, ++i) {
+                const PTile t = list.at(u, i);
                 const int wr = list.wrow(t.nt, (int)rank);
                 for (int kb = 0; kb < nk; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
@@ -181,8 +186,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int u = t0; ok && u < tiles; u += dt) {
-                const PTile t = list.at(u);
+            for (int u = t0, i = 0; ok && u < tiles; u += dt, ++i) {
+                const PTile t = list.at(u, i);
                 const int ar = t.m0 + 128 * (int)rank;
                 for (int kb = 0; kb < nk; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
@@ -259,8 +264,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             int slot = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int u = t0; ok && u < tiles; u += dt) {
-                const PTile t = list.at(u);
+            for (int u = t0, i = 0; ok && u < tiles; u += dt, ++i) {
+                const PTile t = list.at(u, i);
                 int srow[4];  // rows of `a`; -1: past the segment or outside `a`, scale 0
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -324,8 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
         int slot = 0;
         // a wait that gives up raises the abort flag; the warp then runs on over whatever is there
         // (later waits give up at once), meets the named barriers, and stores nothing
-        for (int u = t0; u < tiles; u += dt) {
-            const PTile t = list.at(u);
+        for (int u = t0, i = 0; u < tiles; u += dt, ++i) {
+            const PTile t = list.at(u, i);
             float acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0.f;
@@ -378,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
         if (lane == 0) bulk_wait0();  // this warp's stores are complete
     } else {
         regs_dec<p_other_regs(kGather)>();
-        if (kGather)
+        if constexpr (kGather)
             gather_rows<kPStages>(a, list, (int)rank, (int)threadIdx.x - 640, base, empty_bar, gfull_bar, abort, t0, dt);
     }
 
@@ -398,9 +403,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
     }
 }
 
-template <int kMode, bool kGather>
+template <int kMode, bool kGather, bool kOne>
 cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
-    auto *kernel = fp8_pair_kernel<kMode, kGather>;
+    auto *kernel = fp8_pair_kernel<kMode, kGather, kOne>;
     int unused = 0;
     cudaError_t err = launch_setup_once((const void *)kernel, &unused, [&](int, int *v) -> cudaError_t {
         *v = 1;
@@ -431,9 +436,10 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_fp8_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
-    if (mode == kFp8SwiGlu) return launch_one<kFp8SwiGlu, true>(a, num_sms, s);
-    if (mode == kFp8Y16) return launch_one<kFp8Y16, false>(a, num_sms, s);
-    return a.gather ? launch_one<kFp8Bf16, true>(a, num_sms, s) : launch_one<kFp8Bf16, false>(a, num_sms, s);
+    if (mode == kFp8SwiGlu) return launch_one<kFp8SwiGlu, true, false>(a, num_sms, s);
+    if (mode == kFp8Y16) return launch_one<kFp8Y16, false, false>(a, num_sms, s);
+    if (a.gather) return launch_one<kFp8Bf16, true, false>(a, num_sms, s);
+    return a.expert_off ? launch_one<kFp8Bf16, false, false>(a, num_sms, s) : launch_one<kFp8Bf16, false, true>(a, num_sms, s);
 }
 
 }  // namespace moe

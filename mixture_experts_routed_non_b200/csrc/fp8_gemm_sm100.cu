@@ -44,14 +44,15 @@ struct QCfg {
     static constexpr size_t kScaleOff = kRedOff + kRed;                // [2][kAcc][CN] fp32
     static constexpr size_t kBarOff = kScaleOff + 2 * kAcc * CN * 4;
     static constexpr size_t kMiscOff = kBarOff + 8 * kBars + 8;
-    static constexpr size_t kTableOff = kMiscOff + 16;                 // offsets, then chunks below each expert
+    static constexpr size_t kFirstOff = (kMiscOff + 16 + 15) / 16 * 16;
+    static constexpr size_t kTableOff = kFirstOff + kFListed * 16;     // offsets, then chunks below each expert
     static constexpr size_t kSmem = 1024 + kTableOff + 2 * (kMaxExperts + 1) * 4;
     static_assert(kSmem <= 232448, "shared memory of one CTA (227 KB)");
 };
 
 __device__ __forceinline__ void q_epilogue_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-template <int kMode, bool kGather>
+template <int kMode, bool kGather, bool kOne>
 __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(const __grid_constant__ Fp8GemmArgs a) {
     using C = QCfg<kMode>;
     constexpr int kThreads = kGather ? 320 : 256;
@@ -99,9 +100,11 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
     }
     if (kMode != kFp8Y16) pdl_wait();
     pdl_launch_dependents();
-    load_offsets(a, off_s, kThreads);
-    __syncthreads();
-    if (warp == 0) {
+    if (!kOne) {
+        load_offsets(a, off_s, kThreads);
+        __syncthreads();
+    }
+    if (!kOne && warp == 0) {
         prefix_pieces(off_s, pre_s, E, a.P, CN, lane);
         // nothing to do when the metadata found more pairs than the arrays hold
         if (lane == 0) misc[3] = a.hdr && load_now(&a.hdr->abort) ? 0u : (uint32_t)pre_s[E];
@@ -119,9 +122,11 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
     volatile uint32_t *abort = &misc[1];
     const bool concat = kMode == kFp8SwiGlu && a.layout == MOE_LAYOUT_CONCATENATED;
     const int n_tiles = kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM;
-    const FUnits<CN, kMode> list{off_s, pre_s, E, a.N, n_tiles, concat};
-    const int units = (int)misc[3] * n_tiles;  // below 2^31 (fp8_sizes_ok)
+    FUnits<CN, kMode, kOne> list{off_s,   pre_s,      reinterpret_cast<int4 *>(base_ptr + C::kFirstOff), 0, E, a.N,
+                                 n_tiles, (int)a.P, concat};
+    const int units = (kOne ? ((int)a.P + CN - 1) / CN : (int)misc[3]) * n_tiles;  // below 2^31 (fp8_sizes_ok)
     const int u0 = S > 1 ? (int)blockIdx.x / S : (int)blockIdx.x, du = S > 1 ? (int)gridDim.x / S : (int)gridDim.x;
+    list.fill(units, u0, du);
     // this CTA's share of the scale blocks along K
     const int kb0 = (int)((long long)a.nk * rank / S), kb1 = (int)((long long)a.nk * (rank + 1) / S);
 
@@ -132,8 +137,8 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int u = u0; ok && u < units; u += du) {
-            const FUnit q = list.at(u);
+        for (int u = u0, n = 0; ok && u < units; u += du, ++n) {
+            const FUnit q = list.at(u, n);
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                 if (!ok) break;
@@ -223,8 +228,8 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
         uint32_t it = 0, uc = 0;
         // after a wait that gave up the warps run on over whatever is there, meet the named
         // barriers and store nothing
-        for (int u = u0; u < units; u += du, ++uc) {
-            const FUnit q = list.at(u);
+        for (int u = u0, n = 0; u < units; u += du, ++n, ++uc) {
+            const FUnit q = list.at(u, n);
             FGone<CN> gone;
             if (kGather) gone.load(a, q, lane);
             float acc[C::kAcc][CN];
@@ -291,7 +296,8 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
         }
     } else if (kGather && warp >= 8) {
         // -------------------------------------------------------- row gather
-        gather_chunk_rows<CN, kMode, kStages, C::kStage, C::kStageW>(a, list, units, u0, du, kb0, kb1,
+        if constexpr (kGather)
+            gather_chunk_rows<CN, kMode, kStages, C::kStage, C::kStageW>(a, list, units, u0, du, kb0, kb1,
                                                                      (int)threadIdx.x - 256, base, empty_bar,
                                                                      gfull_bar, abort);
     }
@@ -312,10 +318,10 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
     }
 }
 
-template <int kMode, bool kGather>
+template <int kMode, bool kGather, bool kOne>
 cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     using C = QCfg<kMode>;
-    auto *kernel = fp8_few_any_kernel<kMode, kGather>;
+    auto *kernel = fp8_few_any_kernel<kMode, kGather, kOne>;
     if (!make_few_maps(a, CN, !kGather)) return cudaErrorInvalidValue;
     return launch_few(kernel, a, CN, kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM, kGather ? 320 : 256,
                       C::kSmem, num_sms, s);
@@ -323,13 +329,14 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
 
 // Few rows, a scale in fp32.
 cudaError_t launch_any_few(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
-    if (mode == kFp8SwiGlu) return launch_one<kFp8SwiGlu, true>(a, num_sms, s);
-    if (mode == kFp8Y16) return launch_one<kFp8Y16, false>(a, num_sms, s);
-    return a.gather ? launch_one<kFp8Bf16, true>(a, num_sms, s) : launch_one<kFp8Bf16, false>(a, num_sms, s);
+    if (mode == kFp8SwiGlu) return launch_one<kFp8SwiGlu, true, false>(a, num_sms, s);
+    if (mode == kFp8Y16) return launch_one<kFp8Y16, false, false>(a, num_sms, s);
+    if (a.gather) return launch_one<kFp8Bf16, true, false>(a, num_sms, s);
+    return a.expert_off ? launch_one<kFp8Bf16, false, false>(a, num_sms, s) : launch_one<kFp8Bf16, false, true>(a, num_sms, s);
 }
 
 // How many clusters run at once (few_setup): the same for every few-row kernel, one CTA to an SM.
-cudaError_t any_few_setup(int *fit) { return few_setup(fp8_few_any_kernel<kFp8Bf16, false>, 256, QCfg<kFp8Bf16>::kSmem, fit); }
+cudaError_t any_few_setup(int *fit) { return few_setup(fp8_few_any_kernel<kFp8Bf16, false, true>, 256, QCfg<kFp8Bf16>::kSmem, fit); }
 
 // Which kernel.  Four: few rows or 256-row tiles on CTA pairs, scales by the tensor
 // cores (both e8m0) or in the epilogue (any fp32).  Times below in us, in a graph.

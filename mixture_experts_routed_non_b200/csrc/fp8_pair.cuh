@@ -26,6 +26,7 @@ constexpr int kPGather = 128;               // gather threads of a CTA
 constexpr int kPEpiWarps = 16;
 constexpr uint32_t kPTmem = 512;
 constexpr uint32_t kPStore = 32 * 64;       // per epilogue warp: 32 rows x 32 16-bit columns
+constexpr int kPListed = 64;                // a cluster's first tiles, looked up once
 
 template <int R>
 __device__ __forceinline__ void regs_inc() {
@@ -43,16 +44,47 @@ struct PTile {
 
 // The tile list: row tiles expert by expert, each row tile's weight tiles together
 // (neighbouring clusters share its rows in L2).  off_s and pre_s are shared-memory
-// tables of E + 1 entries.
+// tables of E + 1 entries, first a table of the cluster's first kPListed tiles: a look-up
+// takes some 900 clocks beside the other warps, and every role needs every tile (with 2
+// blocks of K a tile takes 3500).  kOne: one segment of all P rows, no tables.
+template <bool kOne>
 struct PTiles {
     const int *off_s, *pre_s;
-    int E, N, n_tiles;
+    int4 *first;
+    int listed;  // its size: 0 where tiles are few
+    int E, N, n_tiles, P;
     bool concat;
-    __device__ __forceinline__ int count() const { return pre_s[E] * n_tiles; }  // below 2^31 (fp8_sizes_ok)
-    __device__ __forceinline__ PTile at(int u) const {
+    __device__ __forceinline__ int count() const {  // below 2^31 (fp8_sizes_ok)
+        return (kOne ? (P + kPM - 1) / kPM : pre_s[E]) * n_tiles;
+    }
+    // by all threads of the block; t0, dt: the cluster's tiles
+    __device__ __forceinline__ void fill(int t0, int dt) {
+        if (kOne) return;
+        const int n = count(), i = (int)threadIdx.x;
+        listed = n > 2 * dt ? kPListed : 0;
+        if (listed == 0) return;
+        if (i < kPListed && t0 + i * dt < n) {
+            const PTile t = find(t0 + i * dt);
+            first[i] = make_int4(t.e, t.nt, t.m0, t.m_end);
+        }
+        __syncthreads();
+    }
+    // tile u, the cluster's i-th
+    __device__ __forceinline__ PTile at(int u, int i) const {
+        if (kOne || i >= listed) return find(u);
+        const int4 v = first[i];
+        PTile t;
+        t.e = v.x, t.nt = v.y, t.m0 = v.z, t.m_end = v.w;
+        return t;
+    }
+    __device__ __forceinline__ PTile find(int u) const {
         PTile t;
         const int mt = u / n_tiles;
         t.nt = u - mt * n_tiles;
+        if (kOne) {
+            t.e = 0, t.m0 = mt * kPM, t.m_end = P;
+            return t;
+        }
         int lo = 0, hi = E - 1;  // largest e with pre_s[e] <= mt
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -81,12 +113,8 @@ __device__ __forceinline__ T load_now(const T *p) {
 }
 // Segment offsets into off_s, held inside [0, P] whatever the caller's table says.
 __device__ __forceinline__ void load_offsets(const Fp8GemmArgs &a, int *off_s, int threads) {
-    if (a.expert_off) {
-        for (int i = threadIdx.x; i <= a.E; i += threads)
-            off_s[i] = (int)min(max((long long)load_now(a.expert_off + i), 0ll), (long long)a.P);
-    } else if (threadIdx.x < 2) {
-        off_s[threadIdx.x] = threadIdx.x ? (int)a.P : 0;
-    }
+    for (int i = threadIdx.x; i <= a.E; i += threads)
+        off_s[i] = (int)min(max((long long)load_now(a.expert_off + i), 0ll), (long long)a.P);
 }
 // pre_s[e] = pieces of `rows` rows in the experts below e (one converged warp).  Held at
 // the most that ascending offsets can give: a table that goes up and down would count
@@ -146,15 +174,15 @@ __device__ __forceinline__ void store32(const CUtensorMap *map, uint32_t buf, in
 // cost a third to two thirds of the whole product (131072 x 2048 x 1536 over 128
 // experts: 358 us like this, 465 with a zero row, 547 with zero fill).
 template <int kStages, typename Empty, typename Gfull>
-__device__ __forceinline__ void gather_rows(const Fp8GemmArgs &a, const PTiles &list, int rank, int g, uint32_t base,
+__device__ __forceinline__ void gather_rows(const Fp8GemmArgs &a, const PTiles<false> &list, int rank, int g, uint32_t base,
                                             Empty empty_bar, Gfull gfull_bar, volatile uint32_t *abort, int t0,
                                             int dt) {
     const int piece = g & 7, r0 = g >> 3;
     const int tiles = list.count();
     int stage = 0;
     uint32_t phase = 0;
-    for (int u = t0; u < tiles; u += dt) {
-        const PTile t = list.at(u);
+    for (int u = t0, i = 0; u < tiles; u += dt, ++i) {
+        const PTile t = list.at(u, i);
         int row[8];  // -1: not copied
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
