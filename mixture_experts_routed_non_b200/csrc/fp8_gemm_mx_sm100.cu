@@ -52,8 +52,8 @@ struct XCfg {
     static constexpr int kStages = kMode == kFp8SwiGlu ? 6 : 5;
     static constexpr int kBars = 3 * kStages + 3 + 2 * kXSlots;
     static constexpr size_t kStoreOff = (size_t)kStages * kPStage;
-    static constexpr size_t kMaxOff = kStoreOff + (kMode == kFp8SwiGlu ? 0 : kPEpiWarps * kPStore);  // [4][128]
-    static constexpr size_t kBarOff = kMaxOff + 4 * 128 * 4;
+    static constexpr size_t kMaxOff = kStoreOff + (kMode == kFp8SwiGlu ? 0 : kPEpiWarps * kPStore);  // [2][4][128]
+    static constexpr size_t kBarOff = kMaxOff + 2 * 4 * 128 * 4;
     static constexpr size_t kMiscOff = kBarOff + 8 * kBars + 8;
     static constexpr size_t kFirstOff = (kMiscOff + 16 + 15) / 16 * 16;
     static constexpr size_t kTableOff = kFirstOff + kPListed * 16;
@@ -385,7 +385,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
                 acc[j] = __uint_as_float(v0[j]);
                 acc[32 + j] = __uint_as_float(v1[j]);
             }
-            pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s, *abort == 0);
+            pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s + (i & 1) * 512,
+                                        *abort == 0);
         }
         if (lane == 0) bulk_wait0();  // this warp's stores are complete
     } else {

@@ -45,7 +45,7 @@ struct PCfg {
     static constexpr size_t kStoreOff = (size_t)kStages * kPStage;
     static constexpr size_t kScaleOff = kStoreOff + (kMode == kFp8SwiGlu ? 0 : kPEpiWarps * kPStore);
     static constexpr size_t kMaxOff = kScaleOff + kPSlots * kPSlot * 4;  // SwiGlu: [4][128] row maxima
-    static constexpr size_t kBarOff = kMaxOff + 4 * 128 * 4;
+    static constexpr size_t kBarOff = kMaxOff + 2 * 4 * 128 * 4;
     static constexpr size_t kMiscOff = kBarOff + 8 * kBars;
     static constexpr size_t kFirstOff = (kMiscOff + 16 + 15) / 16 * 16;
     static constexpr size_t kTableOff = kFirstOff + kPListed * 16;
@@ -378,7 +378,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
                     sphase ^= 1u;
                 }
             }
-            pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s, *abort == 0);
+            pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s + (i & 1) * 512,
+                                        *abort == 0);
         }
         if (lane == 0) bulk_wait0();  // this warp's stores are complete
     } else {

@@ -36,7 +36,8 @@ template <int R>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
-__device__ __forceinline__ void p_epilogue_bar() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// The four epilogue warps that share a lane quarter's rows.
+__device__ __forceinline__ void p_rows_bar(int q4) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q4) : "memory"); }
 
 struct PTile {
     int e, nt, m0, m_end;
@@ -212,7 +213,8 @@ __device__ __forceinline__ void gather_rows(const Fp8GemmArgs &a, const PTiles<f
 // One epilogue thread's part of a finished tile: row r of this CTA's 128 and 64
 // accumulator columns acc -- the tile's columns [64 cq, 64 cq + 64), or, with
 // concatenated SwiGLU, gates [32 cq, 32 cq + 32) and their ups.  buf: the warp's
-// store buffer; max_s: [4][128] row maxima (SwiGLU).  All 16 warps call it.
+// store buffer; max_s: [4][128] row maxima (SwiGLU), the other of two at the next tile, by whose
+// barrier these have been read.  All 16 warps call it.
 template <int kMode, bool kGather>
 __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t, float (&acc)[64], int rank, int cq,
                                             int q4, int lane, bool concat, uint32_t buf, float *max_s, bool ok) {
@@ -287,7 +289,7 @@ __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t
             m = amax_of(m, h);
         }
         max_s[cq * 128 + r] = m;
-        p_epilogue_bar();
+        p_rows_bar(q4);
         m = fmaxf(fmaxf(max_s[r], max_s[128 + r]), fmaxf(max_s[256 + r], max_s[384 + r]));
         const uint32_t e = e4m3_scale_exp(m);
         const float is = inv_scale_of_exp(e);
@@ -305,7 +307,6 @@ __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t
             }
             if (cq == 0) static_cast<uint8_t *>(a.out_scale)[(size_t)p * (a.N / 256) + t.nt] = (uint8_t)e;
         }
-        p_epilogue_bar();  // max_s has been read
     }
 }
 
