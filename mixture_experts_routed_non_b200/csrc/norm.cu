@@ -22,13 +22,16 @@
 // barriers while that one ends.  Measured back to back (rates of the bytes that have
 // to move): 16384 x 2048 with residual, 8-bit out 44 us (5.4 TB/s; 45 without the early
 // start); 8191 x 7168 with residual, bf16 out 77 us (6.1 TB/s; 79); gradient of 16384
-// x 2048 with dres 48 us (5.6 TB/s; 49), its second kernel included.
+// x 2048 with dres 48 us (5.6 TB/s; 49), its second kernel included.  Without a
+// residual the 8-bit form has half as many bytes to an instruction and is bound by issuing
+// them: 16384 x 2048 29 us (3.5 TB/s; 32 with two products per value and IEEE divisions).
 #include "fp8.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kNMaxT = 512;  // threads per row at most
+constexpr float kLargest = 3.402823466e38f;
 constexpr int kStages = 2;   // of the ring (four: 16384 x 2048 55 us against 43, 8191 x 7168 80 against 75)
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
@@ -132,6 +135,7 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
     __shared__ float red[2][kNMaxT / 32];
     __shared__ uint32_t gave_up;
     const int T = blockDim.x, chunks = a.H / 8;
+    const float per_h = 1.0f / (float)a.H;
     const int blocks = (a.H + kScaleBlock - 1) / kScaleBlock;
     float *my_red[2] = {red[0] + threadIdx.y * (T / 32), red[1] + threadIdx.y * (T / 32)};
     int64_t row0 = (int64_t)blockIdx.x * blockDim.y;  // of the block: every thread makes the same turns
@@ -178,35 +182,53 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
             stage = 0;
             phase ^= 1u;
         }
-        float inv = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+        float inv = rsqrtf(fmaf(ss, per_h, a.eps));  // (within 2 units in the last place)
         if (*(volatile uint32_t *)&gave_up) inv = __uint_as_float(0x7FC00000u);  // a load never came: NaN, not a wrong value
         if (a.inv_rms && threadIdx.x == 0 && row < a.N) a.inv_rms[row] = inv;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = threadIdx.x + i * T;
             const bool in = row < a.N && c < chunks;
-            float f[8], g[8], y[8];
+            float f[8], g[8], v[8];
             unpack8(s[i], f);
             unpack8(w[i], g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = f[j] * g[j] * inv;
-            if (a.y && in) *reinterpret_cast<uint4 *>(a.y + at0 + c * 8) = pack8(y);
+            for (int j = 0; j < 8; ++j) v[j] = f[j] * g[j];
+            if (a.y && in) {
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = v[j] * inv;
+                *reinterpret_cast<uint4 *>(a.y + at0 + c * 8) = pack8(y);
+            }
             if (a.y8) {
-                // 16 consecutive threads hold one block of 128 columns
+                // 16 consecutive threads hold one block of 128 columns.  Its largest |y| is the largest
+                // |s w| times inv (rounding keeps the order), and inv / scale is exact, so that a value
+                // costs one product and the conversion.
                 float m = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    y[j] = inf_to_nan(y[j]);
-                    m = amax_of(m, y[j]);
-                }
+                for (int j = 0; j < 8; ++j) m = amax_of(m, v[j]);
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const uint32_t e = e4m3_scale_exp(m);
-                const float is = inv_scale_of_exp(e);
+                m *= inv;
+                uint32_t e = e4m3_scale_exp(m);
+                float k = inv * inv_scale_of_exp(min(e, 253u));
+                if (__any_sync(0xffffffffu, !(fmaxf(m, k) <= kLargest) || m != m)) {
+                    // an infinity or a NaN among them, or inv / scale past the range: value by value
+                    m = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        v[j] = inf_to_nan(v[j] * inv);
+                        m = amax_of(m, v[j]);
+                    }
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    e = e4m3_scale_exp(m);
+                    k = inv_scale_of_exp(e);
+                }
                 if (in) {
                     *reinterpret_cast<uint2 *>(a.y8 + at0 + c * 8) =
-                        make_uint2(pack_e4m3x4(y[0] * is, y[1] * is, y[2] * is, y[3] * is),
-                                   pack_e4m3x4(y[4] * is, y[5] * is, y[6] * is, y[7] * is));
+                        make_uint2(pack_e4m3x4(v[0] * k, v[1] * k, v[2] * k, v[3] * k),
+                                   pack_e4m3x4(v[4] * k, v[5] * k, v[6] * k, v[7] * k));
                     if ((c & 15) == 0) a.y8_scale[(size_t)row * blocks + (c >> 4)] = (uint8_t)e;
                 }
             }
@@ -223,6 +245,7 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
     __shared__ float red[2][kNMaxT / 32];
     __shared__ uint32_t gave_up;
     const int T = blockDim.x, chunks = a.H / 8;
+    const float per_h = 1.0f / (float)a.H;
     float *my_red[2] = {red[0] + threadIdx.y * (T / 32), red[1] + threadIdx.y * (T / 32)};
     int64_t row0 = (int64_t)blockIdx.x * blockDim.y;
     RowRing<kDres ? 3 : 2> ring;
@@ -271,7 +294,7 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
             phase ^= 1u;
         }
         if (*(volatile uint32_t *)&gave_up) dot = __uint_as_float(0x7FC00000u);  // a load never came: NaN, not a wrong value
-        const float k = inv * inv * (dot / (float)a.H);
+        const float k = inv * inv * (dot * per_h);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = threadIdx.x + i * T;
