@@ -215,11 +215,8 @@ __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q,
                 v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
             }
         };
-        auto add_bias8 = [&](int col, float (&v)[8]) {
-            if (!a.bias) return;
-            const __nv_bfloat16 *br = a.bias + (size_t)q.e * a.N + col;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += __bfloat162float(br[i]);
+        auto bias8 = [&](int col, float (&v)[8]) {
+            if (a.bias) add_bias8(a.bias + (size_t)q.e * a.N + col, bias_aligned(a), v);
         };
         const size_t p = (size_t)q.m0 + jj;
         const bool outside = kGather && (gone.bits[jj >> 5] >> (jj & 31) & 1);  // counts as zeros
@@ -233,7 +230,7 @@ __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q,
             float v[8];
             sum8(0, c8, v);
             keep(v);
-            if (n < a.N) add_bias8(n, v);
+            if (n < a.N) bias8(n, v);
             if (kMode == kFp8Bf16) {
                 if (ok && has && n < a.N)
                     *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + p * a.N + n) =
@@ -265,8 +262,8 @@ __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q,
                 sum8(kAcc - 1, c8, up);
                 keep(g);
                 keep(up);
-                add_bias8(q.nt * 128 + c8, g);
-                add_bias8(a.N / 2 + q.nt * 128 + c8, up);
+                bias8(q.nt * 128 + c8, g);
+                bias8(a.N / 2 + q.nt * 128 + c8, up);
             } else {
                 float x[8], y[8];
                 const int t = c8 >> 6, row = 2 * (c8 & 63);
@@ -274,8 +271,8 @@ __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q,
                 sum8(t, row + 8, y);
                 keep(x);
                 keep(y);
-                add_bias8(q.nt * 256 + 2 * c8, x);
-                add_bias8(q.nt * 256 + 2 * c8 + 8, y);
+                bias8(q.nt * 256 + 2 * c8, x);
+                bias8(q.nt * 256 + 2 * c8 + 8, y);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     g[i] = x[2 * i], up[i] = x[2 * i + 1];

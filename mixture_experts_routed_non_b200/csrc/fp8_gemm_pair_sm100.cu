@@ -15,7 +15,9 @@
 // 2 = TMA of the rows or gather relay, 3 = scale loader, 4-19 = epilogue, 20-23 =
 // row gather (gathered rows only).  The scale loader runs up to eight blocks ahead
 // and leaves sa sw per row and weight half in shared memory, four blocks per slot,
-// so that no epilogue warp waits for global memory.  The relay turns the gather
+// so that no epilogue warp waits for global memory; it copies a group of row scales to
+// shared memory while it hands over the one before (65536 gathered rows over 64 experts,
+// K 2048, N 1536: 287 us; with two dependent loads per group instead 308).  The relay turns the gather
 // threads' copies into one arrival on the MMA's barrier, after the proxy fence that
 // the tensor cores' reads of them need.  Registers are moved to the epilogue warps
 // (setmaxnreg: with gathered rows 4 x 104 + 2 x 32 per thread of the six
@@ -45,7 +47,8 @@ struct PCfg {
     static constexpr size_t kStoreOff = (size_t)kStages * kPStage;
     static constexpr size_t kScaleOff = kStoreOff + (kMode == kFp8SwiGlu ? 0 : kPEpiWarps * kPStore);
     static constexpr size_t kMaxOff = kScaleOff + kPSlots * kPSlot * 4;  // SwiGlu: [4][128] row maxima
-    static constexpr size_t kBarOff = kMaxOff + 2 * 4 * 128 * 4;
+    static constexpr size_t kRawOff = kMaxOff + 2 * 4 * 128 * 4;   // [2][4][128] fp32 row scales
+    static constexpr size_t kBarOff = kRawOff + 2 * 4 * 128 * 4;
     static constexpr size_t kMiscOff = kBarOff + 8 * kBars;
     static constexpr size_t kFirstOff = (kMiscOff + 16 + 15) / 16 * 16;
     static constexpr size_t kTableOff = kFirstOff + kPListed * 16;
@@ -261,50 +264,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             // ------------------------------------------------------ scale loader
             if (kMode == kFp8Y16) pdl_wait();
             const int nb = (a.N + 127) / 128;
-            int slot = 0;
+            const float *as32 = static_cast<const float *>(a.a_scale);
+            // A group of four blocks' fp32 row scales is copied to shared memory (there are too few
+            // registers to hold it) while the group before is multiplied and handed over, a tile's row
+            // numbers are loaded a tile ahead, and lane 4 h + k holds the weight scale of half h, block k.
+            float *raw_s = reinterpret_cast<float *>(base_ptr + C::kRawOff) + lane;  // [2][4 blocks][128 rows]
+            const uint32_t raw_a = base + (uint32_t)C::kRawOff + 4u * lane;
+            PTile t;
+            int srow[4], nrow[4];  // rows of `a`; -1: past the segment or outside `a`, scale 0
+            uint32_t wi = 0, nw = 0, buf = 0, inside = 0;
+            int slot = 0, listed = 0;
             uint32_t phase = 0;
-            bool ok = true;
-            for (int u = t0, i = 0; ok && u < tiles; u += dt, ++i) {
-                const PTile t = list.at(u, i);
-                int srow[4];  // rows of `a`; -1: past the segment or outside `a`, scale 0
+            auto load_rows = [&](int u) {
+                if (u < tiles) t = list.at(u, listed++);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int p = t.m0 + (int)rank * 128 + 32 * i + lane;
-                    srow[i] = p < t.m_end ? (kGather ? __ldg(a.gather + p) : p) : -1;
-                    if (srow[i] >= a.rows) srow[i] = -1;
+                    nrow[i] = u < tiles && p < t.m_end ? (kGather ? __ldg(a.gather + p) : p) : -1;
                 }
-                size_t wi[2];  // (a half past the end of N has no scales: its columns are never stored)
+            };
+            auto enter_tile = [&]() {  // the tile load_rows has just been called for
 #pragma unroll
-                for (int h = 0; h < 2; ++h) wi[h] = ((size_t)t.e * nb + min(list.wrow(t.nt, h) / 128, nb - 1)) * nk;
+                for (int i = 0; i < 4; ++i) srow[i] = nrow[i] < a.rows ? nrow[i] : -1;
+                // (a half past the end of N has no scales: its columns are never stored)
+                wi = (uint32_t)(t.e * nb + min(list.wrow(t.nt, lane >> 2 & 1) / 128, nb - 1));
+            };
+            auto load_group = [&](int kb) {
+                inside = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (srow[i] < 0) continue;
+                    inside |= 1u << i;
+                    if (a.a_f32) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (kb + k < nk)
+                                cp_async_4(raw_a + (buf * 512 + k * 128 + 32 * i) * 4u, as32 + (size_t)srow[i] * nk + kb + k);
+                    } else {  // (beside fp32 scales of the weights)
+                        uint32_t b[4];
+                        load_scale_bits(a.a_scale, 0, (size_t)srow[i] * nk + kb, nk - 1 - kb, b);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) raw_s[buf * 512 + k * 128 + 32 * i] = scale_of_bits(b[k], 0);
+                    }
+                }
+                cp_async_commit();
+                uint32_t w[1];
+                load_scale_bits(a.w_scale, a.w_f32, (size_t)wi * nk + min(kb + (lane & 3), nk - 1), 0, w);
+                nw = w[0];
+            };
+            bool ok = true;
+            if (t0 < tiles) {
+                load_rows(t0);
+                enter_tile();
+                load_group(0);
+                load_rows(t0 + dt);
+            }
+            for (int u = t0; ok && u < tiles; u += dt)
                 for (int kb = 0; kb < nk; kb += 4) {
+                    const float w = scale_of_bits(nw, a.w_f32);
+                    const uint32_t in = inside, at = buf * 512;
+                    buf ^= 1u;
+                    if (kb + 4 < nk) {
+                        load_group(kb + 4);
+                    } else if (u + dt < tiles) {
+                        enter_tile();
+                        load_group(0);
+                        load_rows(u + 2 * dt);
+                    } else {
+                        cp_async_commit();
+                    }
+                    cp_async_wait<1>();  // (each lane reads what it copied itself)
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort));
+                    if (!ok) break;
                     float *sc = scale_s + slot * kPSlot + lane;
 #pragma unroll
-                    for (int k0 = 0; k0 < 4; k0 += 2) {  // two blocks' loads in flight: few registers here
-                        uint32_t rw[2][2], ra[4][2];
-                        const int kk = min(kb + k0, nk - 1), last = nk - 1 - kk;  // behind the end: never used
-                        load_scale_bits(a.w_scale, a.w_f32, wi[0] + kk, last, rw[0]);
-                        load_scale_bits(a.w_scale, a.w_f32, wi[1] + kk, last, rw[1]);
+                    for (int k = 0; k < 4; ++k) {
+                        const float w0 = __shfl_sync(0xffffffffu, w, k), w1 = __shfl_sync(0xffffffffu, w, 4 + k);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            load_scale_bits(a.a_scale, a.a_f32, (size_t)max(srow[i], 0) * nk + kk, last, ra[i]);
-                        if (k0 == 0) {
-                            bool w = true;
-                            if (lane == 0) w = mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort);
-                            ok = __shfl_sync(0xffffffffu, w, 0);
-                            if (!ok) break;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float w0 = scale_of_bits(rw[0][k], a.w_f32), w1 = scale_of_bits(rw[1][k], a.w_f32);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float s = srow[i] >= 0 ? scale_of_bits(ra[i][k], a.a_f32) : 0.f;
-                                sc[(k0 + k) * 256 + 32 * i] = s * w0;
-                                sc[(k0 + k) * 256 + 128 + 32 * i] = s * w1;
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            float s = raw_s[at + k * 128 + 32 * i];
+                            if (!(in >> i & 1u)) s = 0.f;
+                            sc[k * 256 + 32 * i] = s * w0;
+                            sc[k * 256 + 128 + 32 * i] = s * w1;
                         }
                     }
-                    if (!ok) break;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sfull_bar(slot));
                     if (++slot == kPSlots) {
@@ -312,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
                         phase ^= 1u;
                     }
                 }
-            }
+            cp_async_wait_all();
         }
         __syncwarp();
     } else if (warp < 20) {

@@ -210,6 +210,23 @@ __device__ __forceinline__ void gather_rows(const Fp8GemmArgs &a, const PTiles<f
     cp_async_wait_all();
 }
 
+// v[0, 8) += the eight biases from `b` on: one load where they are aligned (aligned is
+// uniform).
+__device__ __forceinline__ void add_bias8(const __nv_bfloat16 *b, bool aligned, float *v) {
+    if (aligned) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(b);
+        v[0] += bf16lo(w.x), v[1] += bf16hi(w.x), v[2] += bf16lo(w.y), v[3] += bf16hi(w.y);
+        v[4] += bf16lo(w.z), v[5] += bf16hi(w.z), v[6] += bf16lo(w.w), v[7] += bf16hi(w.w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += __bfloat162float(b[i]);
+    }
+}
+// (every row and every eighth column of [E, N] keeps the base's alignment: N is a multiple of 8)
+__device__ __forceinline__ bool bias_aligned(const Fp8GemmArgs &a) {
+    return (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0;
+}
+
 // One epilogue thread's part of a finished tile: row r of this CTA's 128 and 64
 // accumulator columns acc -- the tile's columns [64 cq, 64 cq + 64), or, with
 // concatenated SwiGLU, gates [32 cq, 32 cq + 32) and their ups.  buf: the warp's
@@ -234,9 +251,10 @@ __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t
         if (col < a.N) {
             if (a.bias) {
                 const __nv_bfloat16 *br = a.bias + (size_t)t.e * a.N + col;
+                const bool al = bias_aligned(a);
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    if (col + j < a.N) acc[j] += __bfloat162float(br[j]);
+                for (int j = 0; j < 64; j += 8)
+                    if (col + j < a.N) add_bias8(br + j, al, acc + j);
             }
             if (kMode == kFp8Y16) {  // fp16 scaled by a power of two per 32 columns
                 uint32_t exps = 0;
@@ -272,11 +290,10 @@ __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t
         const int hc = t.nt * 128 + cq * 32;  // first h column of this thread
         if (a.bias) {
             const __nv_bfloat16 *br = a.bias + (size_t)t.e * a.N;
+            const bool al = bias_aligned(a);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-                const int col = concat ? (j < 32 ? hc + j : a.N / 2 + hc + j - 32) : 2 * hc + j;
-                acc[j] += __bfloat162float(br[col]);
-            }
+            for (int j = 0; j < 64; j += 8)
+                add_bias8(br + (concat ? (j < 32 ? hc + j : a.N / 2 + hc + j - 32) : 2 * hc + j), al, acc + j);
         }
         float m = 0.f;
 #pragma unroll

@@ -529,3 +529,23 @@ def test_calls_back_to_back_equal_calls_one_by_one():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 256, 264), (90, 7168, 4096), (300, 128, 264), (2000, 256, 520)])
+@pytest.mark.parametrize("scale", [E8, F32])
+def test_bias_at_any_even_address(M, K, N, scale):
+    a, s, w, t, b = _linear_case(M, K, N, scale, scale, True, M + 1)
+    odd = torch.empty(N + 1, dtype=BF16, device="cuda")[1:]
+    odd.copy_(b)
+    assert odd.data_ptr() % 16 == 2
+    assert torch.equal(binding.linear_fp8(a, s, w, t, odd), binding.linear_fp8(a, s, w, t, b))
+
+
+def test_layer_bias_at_any_even_address():
+    for N in (6, 700):
+        x, xs, idx, wt, w1, s1, w2, s2, b1, b2 = _layer_case(N, 256, 128, 5, 2, 0.0, True, E8, E8, 5)
+        odd = [torch.empty(b.numel() + 1, dtype=BF16, device="cuda")[1:].view(b.shape) for b in (b1, b2)]
+        odd[0].copy_(b1), odd[1].copy_(b2)
+        assert odd[0].data_ptr() % 16 == 2
+        assert torch.equal(binding.forward_fp8(x, xs, idx, wt, w1, s1, w2, s2, *odd),
+                           binding.forward_fp8(x, xs, idx, wt, w1, s1, w2, s2, b1, b2))
