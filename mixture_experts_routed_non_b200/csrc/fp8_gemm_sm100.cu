@@ -359,10 +359,13 @@ cudaError_t any_few_setup(int *fit) { return few_setup(fp8_few_any_kernel<kFp8Bf
 //   K 2048, N 1536: rows 128: 8.6, 8.9, 10.3, 10.6; 384: 9.1, 10.2, 12.2, 10.7; 768: 14.1,
 //     10.5, 13.1, 10.9; 1024: 18.7, 15.4, 12.9, 11.0
 //   fp32 scales, K 7168, N 4096: rows 128: 25.6 (chunks of 32), 33.3 (pairs); 256: 47.7, 34.1
-// Segments: only their average is known here.  e8m0, 128 experts, K 768, N 2048, average
-// rows 16 / 32 / 48 / 64 / 96: chunks of 32 37, 47, 62, 76, 105; chunks of 64 37, 38, 41,
-// 60, 81; pairs 50, 52, 53, 54, 56.  (Chunks of 128 only help near 64, by 48 to 54, and not
-// where experts are unequal: 63 to 58.)
+// Segments whose chunks of 32 fit one to an SM however the rows fall (few rows or few
+// experts): the same lines (3 experts of 128 rows, K 1024, N 1024: chunks of 32 7.4, pairs
+// 9.0; fp32 scales 7.8, 10.6).  Other segments: only their average is known here.  e8m0, 128
+// experts, K 768, N 2048, average rows 16 / 32 / 48 / 64 / 96: chunks of 32 38, 46, 62, 75,
+// 101; chunks of 64 37, 39, 41, 54, 71; pairs 49, 50, 51, 51, 53; fp32 scales, rows 24 / 32:
+// chunks of 32 60, 76, pairs 70, 70.  (Chunks of 128 only help near 64, and not where
+// experts are unequal.)
 struct Kernels {
     int chunk;  // rows; 0: pairs
     float start, block;
@@ -370,9 +373,14 @@ struct Kernels {
 constexpr Kernels kE8m0Times[] = {{32, 4.6f, 0.275f}, {64, 5.7f, 0.295f}, {128, 8.0f, 0.325f}, {0, 6.3f, 0.291f}};
 constexpr Kernels kF32Times[] = {{32, 4.0f, 0.385f}, {0, 5.7f, 0.49f}};
 
-float expected_us(const Kernels &k, const Fp8GemmArgs &a, int num_sms, int fit) {
+// Units (tiles) of one segment, or the most that segments can make.
+int64_t units_of(const Kernels &k, const Fp8GemmArgs &a) {
     const int64_t rows = k.chunk ? k.chunk : kPM, cols = k.chunk ? kFM : kPN;
-    const int64_t units = (a.P + rows - 1) / rows * ((a.N + cols - 1) / cols);
+    const int64_t pieces = a.expert_off ? a.P / rows + (a.E < a.P ? a.E : a.P) : (a.P + rows - 1) / rows;
+    return pieces * ((a.N + cols - 1) / cols);
+}
+float expected_us(const Kernels &k, const Fp8GemmArgs &a, int num_sms, int fit) {
+    const int64_t units = units_of(k, a);
     const int S = k.chunk ? few_split(units, a.nk, fit) : 1, at_once = k.chunk ? num_sms / S : num_sms / 2;
     const float waves = (float)((units + at_once - 1) / at_once);
     return k.start + k.block * waves * (float)((a.nk + S - 1) / S) + (S == 1 ? 0.f : S < 8 ? 2.2f : 3.5f);
@@ -384,12 +392,13 @@ cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t 
     if (a.P == 0 || a.N == 0) return cudaSuccess;
     const bool e8m0 = !a.a_f32 && !a.w_f32;
     int chunk = 0;  // rows per chunk of the few-row kernels; 0: pairs
-    if (!a.expert_off) {
+    if (!a.expert_off || units_of(kF32Times[0], a) <= num_sms) {
         int fit = 0;
         const cudaError_t err = any_few_setup(&fit);
         if (err != cudaSuccess) return err;
         float least = 0.f;
         auto pick = [&](const Kernels &k) {
+            if (k.chunk == 128 && a.expert_off) return;
             const float us = expected_us(k, a, num_sms, fit);
             if (least == 0.f || us < least) least = us, chunk = k.chunk;
         };
