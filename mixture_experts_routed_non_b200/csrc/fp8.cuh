@@ -43,7 +43,7 @@ struct Fp8GemmArgs {
     int32_t E, K, N;
     int32_t nk;                 // ceil(K / 128)
     int32_t layout;             // SwiGlu: MOE_LAYOUT_*
-    int32_t split;              // few-row kernel: CTAs that share a unit's K (set by the launch)
+    int32_t split;              // CTAs (few-row kernels) or pairs that share a unit's (tile's) K (set by the launch)
     int32_t pdl;                // launched as a programmatic dependent of the launch before it
 };
 

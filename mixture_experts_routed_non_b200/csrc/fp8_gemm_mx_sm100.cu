@@ -73,8 +73,11 @@ __device__ __forceinline__ void umma_mx_pair(uint32_t d_tmem, uint64_t a_desc, u
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
         : "memory");
 }
-template <int kMode, bool kGather, bool kOne>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 1)
+// kSplit > 1 (one tile per cluster): a cluster of kSplit pairs shares the tile, each pair
+// taking 1/kSplit of K; the pairs then share out the columns, and each adds the others'
+// partial sums of its columns, left in the ring's place, in pair order.
+template <int kMode, bool kGather, bool kOne, int kSplit>
+__global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(x_threads(kGather), 1)
     fp8_mx_pair_kernel(const __grid_constant__ Fp8GemmArgs a) {
     using C = XCfg<kMode>;
     constexpr int kPStages = C::kStages, kPThreads = x_threads(kGather);
@@ -96,7 +99,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     float *max_s = reinterpret_cast<float *>(base_ptr + C::kMaxOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t rank = cluster_ctarank() & 1u, even = cluster_ctarank() & ~1u;  // in the pair; the pair's even CTA
+    const int pi = (int)even >> 1;                                                 // the pair
     const int E = a.E;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPStages; ++s) {
@@ -146,7 +150,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     const bool concat = kMode == kFp8SwiGlu && a.layout == MOE_LAYOUT_CONCATENATED;
     PTiles<kOne> list{off_s, pre_s, reinterpret_cast<int4 *>(base_ptr + C::kFirstOff), 0, E, a.N,
                       (a.N + kPN - 1) / kPN, (int)a.P, concat};
-    const int tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
+    const int tiles = list.count(), t0 = blockIdx.x / (2 * kSplit), dt = gridDim.x / (2 * kSplit);
+    const int kb0 = kSplit == 1 ? 0 : nk * pi / kSplit, kb1 = kSplit == 1 ? nk : nk * (pi + 1) / kSplit;  // of K
     list.fill(t0, dt);
 
     if (warp < 4) {
@@ -154,14 +159,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         if (warp == 0) {
             // ------------------------------------------------ producer: weights
             const bool leader = elect_one();
-            const uint32_t full0 = mapa_shared(full_bar(0), 0);
+            const uint32_t full0 = mapa_shared(full_bar(0), even);
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_parity = 0;
             bool ok = true;
             for (int u = t0, i = 0; ok && u < tiles; u += dt, ++i) {
                 const PTile t = list.at(u, i);
                 const int wr = list.wrow(t.nt, (int)rank);
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                     if (!ok) break;
                     if (leader) {
@@ -189,14 +194,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             // --------------------------------------------------- producer: rows
             if (kMode == kFp8Y16) pdl_wait();
             const bool leader = elect_one();
-            const uint32_t full0 = mapa_shared(full_bar(0), 0);
+            const uint32_t full0 = mapa_shared(full_bar(0), even);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int u = t0, i = 0; ok && u < tiles; u += dt, ++i) {
                 const PTile t = list.at(u, i);
                 const int ar = t.m0 + 128 * (int)rank;
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                     if (!ok) break;
                     if (leader)
@@ -215,28 +220,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             int slot = 0;
             bool ok = true;
             constexpr uint32_t idesc = idesc_mx_e4m3(kPM, kPN);
+            const uint16_t pair_mask = (uint16_t)(0x3u << even);
             // operand descriptors: K-major, 128-byte rows, 8-row atoms 1024 B apart; stages and K
             // steps only move the start address (16-byte units, below 2^14), so the issue loop adds
             const uint64_t desc0 = smem_desc_sw128(base, 16, 1024);
             const bool leader = elect_one();
             for (int u = t0; ok && u < tiles; u += dt, tphase ^= 1u) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(tempty_bar, tphase ^ 1u, abort));
-                for (int kb = 0; ok && kb < nk; ++kb) {
-                    if ((kb & 3) == 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(sfull_bar(slot), sphase, abort));
+                for (int kb = kb0; ok && kb < kb1; ++kb) {
+                    const int k = (kb - kb0) & 3;
+                    if (k == 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(sfull_bar(slot), sphase, abort));
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort)) && ok;
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t da = desc0 + (uint32_t)stage * (kPStage >> 4), db = da + (kPHalf >> 4);
                     const uint32_t sf = tmem_base + kPN + (uint32_t)slot * kXScaleCols;
-                    const uint32_t id = idesc | idesc_byte(kb & 3);
-                    const bool group_end = (kb & 3) == 3 || kb == nk - 1;
+                    const uint32_t id = idesc | idesc_byte(k);
+                    const bool group_end = k == 3 || kb == kb1 - 1;
                     if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_mx_pair(tmem_base, da + 2 * kk, db + 2 * kk, id, sf, sf + 8, (kb | kk) != 0 ? 1u : 0u);
-                        umma_commit_pair_mc(empty_bar(stage), 0x3);
-                        if (kb == nk - 1) umma_commit_pair_mc(tfull_bar, 0x3);
-                        if (group_end) umma_commit_pair_mc(sempty_bar(slot), 0x3);
+                            umma_mx_pair(tmem_base, da + 2 * kk, db + 2 * kk, id, sf, sf + 8, kb > kb0 || kk > 0 ? 1u : 0u);
+                        umma_commit_pair_mc(empty_bar(stage), pair_mask);
+                        if (kb == kb1 - 1) umma_commit_pair_mc(tfull_bar, pair_mask);
+                        if (group_end) umma_commit_pair_mc(sempty_bar(slot), pair_mask);
                     }
                     __syncwarp();
                     if (group_end && ++slot == kXSlots) {
@@ -260,13 +267,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             uint32_t phase = 0;
             bool ok = true;
             for (int u = t0; ok && u < tiles; u += dt)
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait_bounded(gfull_bar(stage), phase, abort)) {
                         ok = false;
                         break;
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive_cluster(mapa_shared(full_bar(stage), 0));
+                    mbar_arrive_cluster(mapa_shared(full_bar(stage), even));
                     if (++stage == kPStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -281,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         const int nb = (a.N + 127) / 128;
         const uint8_t *as = static_cast<const uint8_t *>(a.a_scale), *ws = static_cast<const uint8_t *>(a.w_scale);
         const uint32_t sf0 = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + kPN;
-        const uint32_t sfull0 = mapa_shared(sfull_bar(0), 0);
+        const uint32_t sfull0 = mapa_shared(sfull_bar(0), even);
         int slot = 0;
         uint32_t phase = 0;
         // The words of the next four blocks are loaded before the current four are handed over,
@@ -308,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
             for (int h = 0; h < 2; ++h) wi[h] = ((size_t)t.e * nb + min(list.wrow(t.nt, h) / 128, nb - 1)) * nk;
         };
         auto load_group = [&](int kb) {
-            const int last = nk - 1 - kb;
+            const int last = kb1 - 1 - kb;
             shifts = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)  // (-1: some row's scales, for accumulator rows that are dropped)
@@ -320,21 +327,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         if (t0 < tiles) {
             load_rows(t0);
             enter_tile();
-            load_group(0);
+            load_group(kb0);
             load_rows(t0 + dt);
         }
         for (int u = t0; ok && u < tiles; u += dt) {
-            for (int kb = 0; ok && kb < nk; kb += 4) {
+            for (int kb = kb0; ok && kb < kb1; kb += 4) {
                 uint32_t ca[4], cw[2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) ca[i] = e8m0_word(ra[i][0], ra[i][1], shifts, 5 - i);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) cw[h] = e8m0_word(rw[h][0], rw[h][1], shifts, 1 - h);
-                if (kb + 4 < nk) {
+                if (kb + 4 < kb1) {
                     load_group(kb + 4);
                 } else if (u + dt < tiles) {
                     enter_tile();
-                    load_group(0);
+                    load_group(kb0);
                     load_rows(u + 2 * dt);
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort));
@@ -359,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         // ------------------------------------------------------------ epilogue
         const int q4 = warp & 3, cq = (warp - 8) >> 2;
         const uint32_t buf = base + (uint32_t)C::kStoreOff + (uint32_t)(warp - 8) * kPStore;
-        const uint32_t tempty0 = mapa_shared(tempty_bar, 0);
+        const uint32_t tempty0 = mapa_shared(tempty_bar, even);
         // the warp's two 32-column chunks of the accumulator: its own quarter, or (concatenated
         // SwiGLU) one of the gates and the matching one of the ups
         const int c0 = concat ? 32 * cq : 64 * cq, c1 = concat ? 128 + 32 * cq : 64 * cq + 32;
@@ -385,6 +392,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
                 acc[j] = __uint_as_float(v0[j]);
                 acc[32 + j] = __uint_as_float(v1[j]);
             }
+            if (kSplit > 1) {
+                // [cq][16 groups of four columns][128 rows][4], in the ring: its last MMA has read it
+                const bool mine = cq * kSplit / 4 == pi;
+                const uint32_t part = base + (uint32_t)cq * 32768u + (uint32_t)(32 * q4 + lane) * 16u;
+                if (!mine) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        st_shared_v4(part + j * 2048u, __float_as_uint(acc[4 * j]), __float_as_uint(acc[4 * j + 1]),
+                                     __float_as_uint(acc[4 * j + 2]), __float_as_uint(acc[4 * j + 3]));
+                }
+                cluster_sync_all();
+                if (!mine) continue;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int p = 0; p < kSplit; ++p) {
+                        float4 v = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+                        if (p != pi) v = ld_cluster_f4(mapa_shared(part + j * 2048u, 2 * p + rank));
+                        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                    }
+                    acc[4 * j] = s.x, acc[4 * j + 1] = s.y, acc[4 * j + 2] = s.z, acc[4 * j + 3] = s.w;
+                }
+            }
             pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s + (i & 1) * 512,
                                         *abort == 0);
         }
@@ -393,6 +424,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
         regs_dec<x_other_regs(kGather)>();
         if constexpr (kGather)
             gather_rows<kPStages>(a, list, (int)rank, (int)threadIdx.x - 768, base, empty_bar, gfull_bar, abort, t0, dt);
+    }
+
+    if (kSplit > 1 && (warp < 8 || warp >= 24)) {
+        __syncwarp();
+        cluster_sync_all();  // the epilogue's, behind which the partial sums are there
     }
 
     // ---------------------------------------------------------------- teardown
@@ -411,9 +447,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(kGather), 
     }
 }
 
-template <int kMode, bool kGather, bool kOne>
+template <int kMode, bool kGather, bool kOne, int kSplit>
 cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
-    auto *kernel = fp8_mx_pair_kernel<kMode, kGather, kOne>;
+    auto *kernel = fp8_mx_pair_kernel<kMode, kGather, kOne, kSplit>;
     int unused = 0;
     cudaError_t err = launch_setup_once((const void *)kernel, &unused, [&](int, int *v) -> cudaError_t {
         *v = 1;
@@ -435,19 +471,23 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     if (kMode != kFp8SwiGlu && !make_map_out16(&a.tmap_out, a.out, (uint64_t)a.N, (uint64_t)a.P))
         return cudaErrorInvalidValue;
     const int n_tiles = (a.N + kPN - 1) / kPN;
-    // no more row tiles than P / 256 and one begun per expert
-    const int64_t tiles = (a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
-    const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
-    return launch_maybe_pdl(kernel, dim3(2 * clusters), dim3(x_threads(kGather)), XCfg<kMode>::kSmem, s, a.pdl != 0, a);
+    // one segment: its row tiles; else no more than P / 256 and one begun per expert
+    const int64_t tiles = (kOne ? (a.P + kPM - 1) / kPM : a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
+    // (split: one tile to a cluster)
+    const int clusters = (int)(kSplit > 1 || tiles < num_sms / 2 ? tiles : num_sms / 2);
+    return launch_maybe_pdl(kernel, dim3(2 * kSplit * clusters), dim3(x_threads(kGather)), XCfg<kMode>::kSmem, s, a.pdl != 0, a);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_mx_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
-    if (mode == kFp8SwiGlu) return launch_one<kFp8SwiGlu, true, false>(a, num_sms, s);
-    if (mode == kFp8Y16) return launch_one<kFp8Y16, false, false>(a, num_sms, s);
-    if (a.gather) return launch_one<kFp8Bf16, true, false>(a, num_sms, s);
-    return a.expert_off ? launch_one<kFp8Bf16, false, false>(a, num_sms, s) : launch_one<kFp8Bf16, false, true>(a, num_sms, s);
+    if (mode == kFp8SwiGlu) return launch_one<kFp8SwiGlu, true, false, 1>(a, num_sms, s);
+    if (mode == kFp8Y16) return launch_one<kFp8Y16, false, false, 1>(a, num_sms, s);
+    if (a.gather) return launch_one<kFp8Bf16, true, false, 1>(a, num_sms, s);
+    if (a.expert_off) return launch_one<kFp8Bf16, false, false, 1>(a, num_sms, s);
+    if (a.split == 4) return launch_one<kFp8Bf16, false, true, 4>(a, num_sms, s);
+    if (a.split == 2) return launch_one<kFp8Bf16, false, true, 2>(a, num_sms, s);
+    return launch_one<kFp8Bf16, false, true, 1>(a, num_sms, s);
 }
 
 }  // namespace moe

@@ -349,13 +349,17 @@ cudaError_t any_few_setup(int *fit) { return few_setup(fp8_few_any_kernel<kFp8Bf
 //                         64     5.7  0.295
 //                        128     8.0  0.325
 //     pairs                      6.3  0.291                   5.7  0.49
-//   (pairs with e8m0: 5 % above the fit, 6.0 and 0.277.  Where others come as near, rows whose
+//     2 (4) pairs to a tile   9.3 (10.3)  0.291, of their part of K
+//   (one pair with e8m0: 5 % above the fit, 6.0 and 0.277.  Where others come as near, rows whose
 //   pitch is no multiple of 32 bytes decide: 600 x 2992 x 1000 12.5 in chunks of 64, 15.0 in pairs.)
 //   Measured, K 7168, N 4096    rows   16    48    96   128   256   384   512
 //     chunks of 32                   10.0  14.2  20.0  20.0  35.6  51.2  66.3
 //     chunks of 64                         12.4  16.1  16.2  22.1  38.6  38.8
 //     chunks of 128                        13.2  14.4  15.5  19.6  25.8  26.0
 //     pairs                                21.4  21.8  22.1  22.3  22.7  23.7
+//     two pairs                                                          18.5
+//   K 7168, rows 256, N 3584: chunks of 128 18.3; pairs 21.2, two 16.5, four 14.7; K 2048, rows
+//     1000, N 1536: pairs 10.1, two 11.2
 //   K 2048, N 1536: rows 128: 8.6, 8.9, 10.3, 10.6; 384: 9.1, 10.2, 12.2, 10.7; 768: 14.1,
 //     10.5, 13.1, 10.9; 1024: 18.7, 15.4, 12.9, 11.0
 //   fp32 scales, K 7168, N 4096: rows 128: 25.6 (chunks of 32), 33.3 (pairs); 256: 47.7, 34.1
@@ -368,10 +372,12 @@ cudaError_t any_few_setup(int *fit) { return few_setup(fp8_few_any_kernel<kFp8Bf
 // experts are unequal.)
 struct Kernels {
     int chunk;  // rows; 0: pairs
+    int pairs;  // that share a tile's K
     float start, block;
 };
-constexpr Kernels kE8m0Times[] = {{32, 4.6f, 0.275f}, {64, 5.7f, 0.295f}, {128, 8.0f, 0.325f}, {0, 6.3f, 0.291f}};
-constexpr Kernels kF32Times[] = {{32, 4.0f, 0.385f}, {0, 5.7f, 0.49f}};
+constexpr Kernels kE8m0Times[] = {{32, 0, 4.6f, 0.275f}, {64, 0, 5.7f, 0.295f}, {128, 0, 8.0f, 0.325f},
+                                  {0, 1, 6.3f, 0.291f},  {0, 2, 9.3f, 0.291f},  {0, 4, 10.3f, 0.291f}};
+constexpr Kernels kF32Times[] = {{32, 0, 4.0f, 0.385f}, {0, 1, 5.7f, 0.49f}};
 
 // Units (tiles) of one segment, or the most that segments can make.
 int64_t units_of(const Kernels &k, const Fp8GemmArgs &a) {
@@ -381,9 +387,9 @@ int64_t units_of(const Kernels &k, const Fp8GemmArgs &a) {
 }
 float expected_us(const Kernels &k, const Fp8GemmArgs &a, int num_sms, int fit) {
     const int64_t units = units_of(k, a);
-    const int S = k.chunk ? few_split(units, a.nk, fit) : 1, at_once = k.chunk ? num_sms / S : num_sms / 2;
+    const int S = k.chunk ? few_split(units, a.nk, fit) : k.pairs, at_once = k.chunk ? num_sms / S : num_sms / 2;
     const float waves = (float)((units + at_once - 1) / at_once);
-    return k.start + k.block * waves * (float)((a.nk + S - 1) / S) + (S == 1 ? 0.f : S < 8 ? 2.2f : 3.5f);
+    return k.start + k.block * waves * (float)((a.nk + S - 1) / S) + (S == 1 || !k.chunk ? 0.f : S < 8 ? 2.2f : 3.5f);
 }
 
 }  // namespace
@@ -398,9 +404,11 @@ cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t 
         if (err != cudaSuccess) return err;
         float least = 0.f;
         auto pick = [&](const Kernels &k) {
-            if (k.chunk == 128 && a.expert_off) return;
+            if ((k.chunk == 128 || k.pairs > 1) && a.expert_off) return;
+            // pairs share a tile where all their clusters run at once and each keeps a group of four blocks
+            if (k.pairs > 1 && (a.nk < 4 * k.pairs || units_of(k, a) > ((fit >> (4 * k.pairs)) & 255))) return;
             const float us = expected_us(k, a, num_sms, fit);
-            if (least == 0.f || us < least) least = us, chunk = k.chunk;
+            if (least == 0.f || us < least) least = us, chunk = k.chunk, a.split = k.pairs;
         };
         if (e8m0) for (const Kernels &k : kE8m0Times) pick(k);
         else for (const Kernels &k : kF32Times) pick(k);

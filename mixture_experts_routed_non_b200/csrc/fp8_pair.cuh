@@ -39,6 +39,16 @@ __device__ __forceinline__ void regs_dec() {
 // The four epilogue warps that share a lane quarter's rows.
 __device__ __forceinline__ void p_rows_bar(int q4) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q4) : "memory"); }
 
+// Four floats of another CTA's shared memory.
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+
 struct PTile {
     int e, nt, m0, m_end;
 };

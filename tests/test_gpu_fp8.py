@@ -464,6 +464,20 @@ def test_linear_of_a_hundred_or_two_rows_on_a_large_matrix(M, K, N, bias):
     assert bool((out[M:] == 9).all())
 
 
+@pytest.mark.parametrize("M,K,N", [(512, 7168, 4096), (256, 7168, 3584), (700, 4640, 888), (1371, 5584, 888), (513, 3600, 264)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_linear_of_few_tiles_and_a_long_k(M, K, N, bias):
+    a, s, w, t, b = _linear_case(M, K, N, E8, E8, bias, M + K)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((M + 3, N), 9.0, dtype=BF16, device="cuda")
+    first = binding.linear_fp8(a, s, w, t, b, out=out[:M], err=err).clone()
+    y, tol = ref.product(ref.values(a, s), ref.weight_values(w, t), b)
+    ref.check(first, y, tol)
+    assert bool((out[M:] == 9).all()) and int(err) == 0
+    for _ in range(3):  # whatever the pairs' timing
+        assert torch.equal(first, binding.linear_fp8(a, s, w, t, b))
+
+
 @pytest.mark.parametrize("M,K,N", [(96, 2048, 1536), (128, 7168, 512), (256, 7168, 512), (33, 1024, 1200)])
 @pytest.mark.parametrize("scale", [E8, F32])
 def test_linear_split_over_clusters(M, K, N, scale):
