@@ -73,9 +73,7 @@ __device__ __forceinline__ void umma_mx_pair(uint32_t d_tmem, uint64_t a_desc, u
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
         : "memory");
 }
-// kSplit > 1 (one tile per cluster): a cluster of kSplit pairs shares the tile, each pair
-// taking 1/kSplit of K; the pairs then share out the columns, and each adds the others'
-// partial sums of its columns, left in the ring's place, in pair order.
+// kSplit > 1 (one tile per cluster): kSplit pairs share the tile's K (pair_share).
 template <int kMode, bool kGather, bool kOne, int kSplit>
 __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(x_threads(kGather), 1)
     fp8_mx_pair_kernel(const __grid_constant__ Fp8GemmArgs a) {
@@ -392,30 +390,7 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(x_threads(k
                 acc[j] = __uint_as_float(v0[j]);
                 acc[32 + j] = __uint_as_float(v1[j]);
             }
-            if (kSplit > 1) {
-                // [cq][16 groups of four columns][128 rows][4], in the ring: its last MMA has read it
-                const bool mine = cq * kSplit / 4 == pi;
-                const uint32_t part = base + (uint32_t)cq * 32768u + (uint32_t)(32 * q4 + lane) * 16u;
-                if (!mine) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        st_shared_v4(part + j * 2048u, __float_as_uint(acc[4 * j]), __float_as_uint(acc[4 * j + 1]),
-                                     __float_as_uint(acc[4 * j + 2]), __float_as_uint(acc[4 * j + 3]));
-                }
-                cluster_sync_all();
-                if (!mine) continue;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int p = 0; p < kSplit; ++p) {
-                        float4 v = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-                        if (p != pi) v = ld_cluster_f4(mapa_shared(part + j * 2048u, 2 * p + rank));
-                        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-                    }
-                    acc[4 * j] = s.x, acc[4 * j + 1] = s.y, acc[4 * j + 2] = s.z, acc[4 * j + 3] = s.w;
-                }
-            }
+            if (kSplit > 1 && !pair_share<kSplit>(acc, base, (int)rank, pi, cq, q4, lane)) continue;
             pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s + (i & 1) * 512,
                                         *abort == 0);
         }

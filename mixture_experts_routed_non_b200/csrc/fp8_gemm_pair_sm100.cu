@@ -7,7 +7,7 @@
 // fill the other accumulator.  At the tensor cores' full rate a block takes 512
 // clocks; what bounds it here is the hand-over of an accumulator, about 1200
 // clocks of latency (barrier, TMEM load, arithmetic, barrier, in turn) that four
-// warps per scheduler hide in part (8192 x 7168 x 4096: 240 us = 2.0 PFLOP/s; with
+// warps per scheduler hide in part (8192 x 7168 x 4096: 226 us = 2.1 PFLOP/s; with
 // eight warps of 128 columns 340, with power-of-two scales, which need none of
 // this, 141).
 //
@@ -65,8 +65,9 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, u
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-template <int kMode, bool kGather, bool kOne>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 1)
+// kSplit > 1 (one tile per cluster): kSplit pairs share the tile's K (pair_share).
+template <int kMode, bool kGather, bool kOne, int kSplit>
+__global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(p_threads(kGather), 1)
     fp8_pair_kernel(const __grid_constant__ Fp8GemmArgs a) {
     using C = PCfg<kMode>;
     constexpr int kPStages = C::kStages, kPThreads = p_threads(kGather);
@@ -90,7 +91,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
     float *max_s = reinterpret_cast<float *>(base_ptr + C::kMaxOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t rank = cluster_ctarank() & 1u, even = cluster_ctarank() & ~1u;  // in the pair; the pair's even CTA
+    const int pi = (int)even >> 1;                                                 // the pair
     const int E = a.E;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPStages; ++s) {
@@ -142,7 +144,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
     const bool concat = kMode == kFp8SwiGlu && a.layout == MOE_LAYOUT_CONCATENATED;
     PTiles<kOne> list{off_s, pre_s, reinterpret_cast<int4 *>(base_ptr + C::kFirstOff), 0, E, a.N,
                       (a.N + kPN - 1) / kPN, (int)a.P, concat};
-    const int tiles = list.count(), t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
+    const int tiles = list.count(), t0 = blockIdx.x / (2 * kSplit), dt = gridDim.x / (2 * kSplit);
+    const int kb0 = kSplit == 1 ? 0 : nk * pi / kSplit, kb1 = kSplit == 1 ? nk : nk * (pi + 1) / kSplit;  // of K
     list.fill(t0, dt);
 
     if (warp < 4) {
@@ -150,14 +153,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
         if (warp == 0) {
             // ------------------------------------------------ producer: weights
             const bool leader = elect_one();
-            const uint32_t full0 = mapa_shared(full_bar(0), 0);
+            const uint32_t full0 = mapa_shared(full_bar(0), even);
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_parity = 0;
             bool ok = true;
             for (int u = t0, i = 0; ok && u < tiles; u += dt, ++i) {
                 const PTile t = list.at(u, i);
                 const int wr = list.wrow(t.nt, (int)rank);
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                     if (!ok) break;
                     if (leader) {
@@ -185,14 +188,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             // --------------------------------------------------- producer: rows
             if (kMode == kFp8Y16) pdl_wait();
             const bool leader = elect_one();
-            const uint32_t full0 = mapa_shared(full_bar(0), 0);
+            const uint32_t full0 = mapa_shared(full_bar(0), even);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int u = t0, i = 0; ok && u < tiles; u += dt, ++i) {
                 const PTile t = list.at(u, i);
                 const int ar = t.m0 + 128 * (int)rank;
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort));
                     if (!ok) break;
                     if (leader)
@@ -210,12 +213,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             uint32_t phase = 0, it = 0;
             bool ok = true;
             constexpr uint32_t idesc = idesc_e4m3_f32(kPM, kPN);
+            const uint16_t pair_mask = (uint16_t)(0x3u << even);
             // operand descriptors: K-major, 128-byte rows, 8-row atoms 1024 B apart; stages and K
             // steps only move the start address (16-byte units, below 2^14), so the issue loop adds
             const uint64_t desc0 = smem_desc_sw128(base, 16, 1024);
             const bool leader = elect_one();
             for (int u = t0; ok && u < tiles; u += dt) {
-                for (int kb = 0; kb < nk; ++kb, ++it) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const uint32_t b = it & 1u;
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort)) &&
                          __all_sync(0xffffffffu, mbar_wait_bounded(tempty_bar(b), ((it >> 1) & 1u) ^ 1u, abort));
@@ -227,8 +231,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_f8_pair(d, da + 2 * kk, db + 2 * kk, idesc, kk != 0 ? 1u : 0u);
-                        umma_commit_pair_mc(tfull_bar(b), 0x3);
-                        umma_commit_pair_mc(empty_bar(stage), 0x3);
+                        umma_commit_pair_mc(tfull_bar(b), pair_mask);
+                        umma_commit_pair_mc(empty_bar(stage), pair_mask);
                     }
                     __syncwarp();
                     if (++stage == kPStages) {
@@ -248,13 +252,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             uint32_t phase = 0;
             bool ok = true;
             for (int u = t0; ok && u < tiles; u += dt)
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait_bounded(gfull_bar(stage), phase, abort)) {
                         ok = false;
                         break;
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive_cluster(mapa_shared(full_bar(stage), 0));
+                    mbar_arrive_cluster(mapa_shared(full_bar(stage), even));
                     if (++stage == kPStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -298,37 +302,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
                     if (a.a_f32) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (kb + k < nk)
+                            if (kb + k < kb1)
                                 cp_async_4(raw_a + (buf * 512 + k * 128 + 32 * i) * 4u, as32 + (size_t)srow[i] * nk + kb + k);
                     } else {  // (beside fp32 scales of the weights)
                         uint32_t b[4];
-                        load_scale_bits(a.a_scale, 0, (size_t)srow[i] * nk + kb, nk - 1 - kb, b);
+                        load_scale_bits(a.a_scale, 0, (size_t)srow[i] * nk + kb, kb1 - 1 - kb, b);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) raw_s[buf * 512 + k * 128 + 32 * i] = scale_of_bits(b[k], 0);
                     }
                 }
                 cp_async_commit();
                 uint32_t w[1];
-                load_scale_bits(a.w_scale, a.w_f32, (size_t)wi * nk + min(kb + (lane & 3), nk - 1), 0, w);
+                load_scale_bits(a.w_scale, a.w_f32, (size_t)wi * nk + min(kb + (lane & 3), kb1 - 1), 0, w);
                 nw = w[0];
             };
             bool ok = true;
             if (t0 < tiles) {
                 load_rows(t0);
                 enter_tile();
-                load_group(0);
+                load_group(kb0);
                 load_rows(t0 + dt);
             }
             for (int u = t0; ok && u < tiles; u += dt)
-                for (int kb = 0; kb < nk; kb += 4) {
+                for (int kb = kb0; kb < kb1; kb += 4) {
                     const float w = scale_of_bits(nw, a.w_f32);
                     const uint32_t in = inside, at = buf * 512;
                     buf ^= 1u;
-                    if (kb + 4 < nk) {
+                    if (kb + 4 < kb1) {
                         load_group(kb + 4);
                     } else if (u + dt < tiles) {
                         enter_tile();
-                        load_group(0);
+                        load_group(kb0);
                         load_rows(u + 2 * dt);
                     } else {
                         cp_async_commit();
@@ -363,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
         // ------------------------------------------------------------ epilogue
         const int q4 = warp & 3, cq = (warp - 4) >> 2;
         const uint32_t buf = base + (uint32_t)C::kStoreOff + (uint32_t)(warp - 4) * kPStore;
-        const uint32_t tempty0 = mapa_shared(tempty_bar(0), 0), tempty1 = mapa_shared(tempty_bar(1), 0);
+        const uint32_t tempty0 = mapa_shared(tempty_bar(0), even), tempty1 = mapa_shared(tempty_bar(1), even);
         // the warp's two 32-column chunks of the accumulator: its own quarter, or (concatenated
         // SwiGLU) one of the gates and the matching one of the ups
         const int c0 = concat ? 32 * cq : 64 * cq, c1 = concat ? 128 + 32 * cq : 64 * cq + 32;
@@ -377,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
             float acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0.f;
-            for (int kb = 0; kb < nk; kb += 4) {
+            for (int kb = kb0; kb < kb1; kb += 4) {
                 mbar_wait_bounded(sfull_bar(slot), sphase, abort);
                 __syncwarp();
                 float f0[4], f1[4];
@@ -388,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (kb + k < nk) {
+                    if (kb + k < kb1) {
                         const uint32_t b = it & 1u;
                         mbar_wait_bounded(tfull_bar(b), (it >> 1) & 1u, abort);
                         ++it;
@@ -421,6 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
                     sphase ^= 1u;
                 }
             }
+            if (kSplit > 1 && !pair_share<kSplit>(acc, base, (int)rank, pi, cq, q4, lane)) continue;
             pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s + (i & 1) * 512,
                                         *abort == 0);
         }
@@ -429,6 +434,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
         regs_dec<p_other_regs(kGather)>();
         if constexpr (kGather)
             gather_rows<kPStages>(a, list, (int)rank, (int)threadIdx.x - 640, base, empty_bar, gfull_bar, abort, t0, dt);
+    }
+
+    if (kSplit > 1 && (warp < 4 || warp >= 20)) {
+        __syncwarp();
+        cluster_sync_all();  // the epilogue's, behind which the partial sums are there
     }
 
     // ---------------------------------------------------------------- teardown
@@ -447,9 +457,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(p_threads(kGather), 
     }
 }
 
-template <int kMode, bool kGather, bool kOne>
+template <int kMode, bool kGather, bool kOne, int kSplit>
 cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
-    auto *kernel = fp8_pair_kernel<kMode, kGather, kOne>;
+    auto *kernel = fp8_pair_kernel<kMode, kGather, kOne, kSplit>;
     int unused = 0;
     cudaError_t err = launch_setup_once((const void *)kernel, &unused, [&](int, int *v) -> cudaError_t {
         *v = 1;
@@ -471,19 +481,23 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     if (kMode != kFp8SwiGlu && !make_map_out16(&a.tmap_out, a.out, (uint64_t)a.N, (uint64_t)a.P))
         return cudaErrorInvalidValue;
     const int n_tiles = (a.N + kPN - 1) / kPN;
-    // no more row tiles than P / 256 and one begun per expert
-    const int64_t tiles = (a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
-    const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
-    return launch_maybe_pdl(kernel, dim3(2 * clusters), dim3(p_threads(kGather)), PCfg<kMode>::kSmem, s, a.pdl != 0, a);
+    // one segment: its row tiles; else no more than P / 256 and one begun per expert
+    const int64_t tiles = (kOne ? (a.P + kPM - 1) / kPM : a.P / kPM + (a.E < a.P ? a.E : a.P)) * n_tiles;
+    // (split: one tile to a cluster)
+    const int clusters = (int)(kSplit > 1 || tiles < num_sms / 2 ? tiles : num_sms / 2);
+    return launch_maybe_pdl(kernel, dim3(2 * kSplit * clusters), dim3(p_threads(kGather)), PCfg<kMode>::kSmem, s, a.pdl != 0, a);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
-    if (mode == kFp8SwiGlu) return launch_one<kFp8SwiGlu, true, false>(a, num_sms, s);
-    if (mode == kFp8Y16) return launch_one<kFp8Y16, false, false>(a, num_sms, s);
-    if (a.gather) return launch_one<kFp8Bf16, true, false>(a, num_sms, s);
-    return a.expert_off ? launch_one<kFp8Bf16, false, false>(a, num_sms, s) : launch_one<kFp8Bf16, false, true>(a, num_sms, s);
+    if (mode == kFp8SwiGlu) return launch_one<kFp8SwiGlu, true, false, 1>(a, num_sms, s);
+    if (mode == kFp8Y16) return launch_one<kFp8Y16, false, false, 1>(a, num_sms, s);
+    if (a.gather) return launch_one<kFp8Bf16, true, false, 1>(a, num_sms, s);
+    if (a.expert_off) return launch_one<kFp8Bf16, false, false, 1>(a, num_sms, s);
+    if (a.split == 4) return launch_one<kFp8Bf16, false, true, 4>(a, num_sms, s);
+    if (a.split == 2) return launch_one<kFp8Bf16, false, true, 2>(a, num_sms, s);
+    return launch_one<kFp8Bf16, false, true, 1>(a, num_sms, s);
 }
 
 }  // namespace moe

@@ -349,7 +349,7 @@ cudaError_t any_few_setup(int *fit) { return few_setup(fp8_few_any_kernel<kFp8Bf
 //                         64     5.7  0.295
 //                        128     8.0  0.325
 //     pairs                      6.3  0.291                   5.7  0.49
-//     2 (4) pairs to a tile   9.3 (10.3)  0.291, of their part of K
+//     2 (4) pairs to a tile   9.3 (10.3)  0.291              9.5 (11.0)  0.49, of their part of K
 //   (one pair with e8m0: 5 % above the fit, 6.0 and 0.277.  Where others come as near, rows whose
 //   pitch is no multiple of 32 bytes decide: 600 x 2992 x 1000 12.5 in chunks of 64, 15.0 in pairs.)
 //   Measured, K 7168, N 4096    rows   16    48    96   128   256   384   512
@@ -362,7 +362,8 @@ cudaError_t any_few_setup(int *fit) { return few_setup(fp8_few_any_kernel<kFp8Bf
 //     1000, N 1536: pairs 10.1, two 11.2
 //   K 2048, N 1536: rows 128: 8.6, 8.9, 10.3, 10.6; 384: 9.1, 10.2, 12.2, 10.7; 768: 14.1,
 //     10.5, 13.1, 10.9; 1024: 18.7, 15.4, 12.9, 11.0
-//   fp32 scales, K 7168, N 4096: rows 128: 25.6 (chunks of 32), 33.3 (pairs); 256: 47.7, 34.1
+//   fp32 scales, K 7168, N 4096: rows 128: 25.6 (chunks of 32), 33.3 (pairs); 256: 47.7,
+//     34.1; 512: 90.9, 33.0, two pairs 24.3; K 7168, rows 256, N 3584: 46.8, 32.5, 22.8, four 18.2
 // Segments whose chunks of 32 fit one to an SM however the rows fall (few rows or few
 // experts): the same lines (3 experts of 128 rows, K 1024, N 1024: chunks of 32 7.4, pairs
 // 9.0; fp32 scales 7.8, 10.6).  Other segments: only their average is known here.  e8m0, 128
@@ -377,7 +378,7 @@ struct Kernels {
 };
 constexpr Kernels kE8m0Times[] = {{32, 0, 4.6f, 0.275f}, {64, 0, 5.7f, 0.295f}, {128, 0, 8.0f, 0.325f},
                                   {0, 1, 6.3f, 0.291f},  {0, 2, 9.3f, 0.291f},  {0, 4, 10.3f, 0.291f}};
-constexpr Kernels kF32Times[] = {{32, 0, 4.0f, 0.385f}, {0, 1, 5.7f, 0.49f}};
+constexpr Kernels kF32Times[] = {{32, 0, 4.0f, 0.385f}, {0, 1, 5.7f, 0.49f}, {0, 2, 9.5f, 0.49f}, {0, 4, 11.0f, 0.49f}};
 
 // Units (tiles) of one segment, or the most that segments can make.
 int64_t units_of(const Kernels &k, const Fp8GemmArgs &a) {

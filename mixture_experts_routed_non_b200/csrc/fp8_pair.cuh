@@ -220,6 +220,39 @@ __device__ __forceinline__ void gather_rows(const Fp8GemmArgs &a, const PTiles<f
     cp_async_wait_all();
 }
 
+// A tile whose K is shared by kSplit pairs, a cluster: each pair has the sums of its part of K.
+// The pairs share out the columns; each adds the others' sums of its columns, left in shared
+// memory in the place of the ring (whose last MMA has read it), in pair order.  False: this
+// warp's columns are another pair's.  All threads of the cluster meet in it once, those of
+// other warps in a cluster_sync_all() of their own.
+template <int kSplit>
+__device__ __forceinline__ bool pair_share(float (&acc)[64], uint32_t ring, int rank, int pi, int cq, int q4, int lane) {
+    const bool mine = cq * kSplit / 4 == pi;
+    // [cq][16 groups of four columns][128 rows][4]
+    const uint32_t part = ring + (uint32_t)cq * 32768u + (uint32_t)(32 * q4 + lane) * 16u;
+    if (!mine) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            st_shared_v4(part + j * 2048u, __float_as_uint(acc[4 * j]), __float_as_uint(acc[4 * j + 1]),
+                         __float_as_uint(acc[4 * j + 2]), __float_as_uint(acc[4 * j + 3]));
+    }
+    __syncwarp();
+    cluster_sync_all();
+    if (!mine) return false;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < kSplit; ++p) {
+            float4 v = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+            if (p != pi) v = ld_cluster_f4(mapa_shared(part + j * 2048u, (uint32_t)(2 * p + rank)));
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        acc[4 * j] = s.x, acc[4 * j + 1] = s.y, acc[4 * j + 2] = s.z, acc[4 * j + 3] = s.w;
+    }
+    return true;
+}
+
 // v[0, 8) += the eight biases from `b` on: one load where they are aligned (aligned is
 // uniform).
 __device__ __forceinline__ void add_bias8(const __nv_bfloat16 *b, bool aligned, float *v) {

@@ -465,9 +465,9 @@ def test_linear_of_a_hundred_or_two_rows_on_a_large_matrix(M, K, N, bias):
 
 
 @pytest.mark.parametrize("M,K,N", [(512, 7168, 4096), (256, 7168, 3584), (700, 4640, 888), (1371, 5584, 888), (513, 3600, 264)])
-@pytest.mark.parametrize("bias", [False, True])
-def test_linear_of_few_tiles_and_a_long_k(M, K, N, bias):
-    a, s, w, t, b = _linear_case(M, K, N, E8, E8, bias, M + K)
+@pytest.mark.parametrize("bias,sa,sw", [(False, E8, E8), (True, E8, E8), (True, F32, F32), (False, E8, F32), (False, F32, E8)])
+def test_linear_of_few_tiles_and_a_long_k(M, K, N, bias, sa, sw):
+    a, s, w, t, b = _linear_case(M, K, N, sa, sw, bias, M + K)
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     out = torch.full((M + 3, N), 9.0, dtype=BF16, device="cuda")
     first = binding.linear_fp8(a, s, w, t, b, out=out[:M], err=err).clone()
