@@ -884,15 +884,17 @@ def _need_dim(t: torch.Tensor, name: str, dim: int):
 
 
 def _need_scale(t: torch.Tensor, name: str, shape, device) -> int:
-    if t.dtype not in _SCALE_DTYPES:
-        raise TypeError(f"{name}: expected float8_e8m0fnu or float32, got {t.dtype}")
-    _ok(t, name, t.dtype, shape, device)
-    return _SCALE_DTYPES[t.dtype]
+    dtype = t.dtype
+    if not (dtype in _SCALE_DTYPES and t.shape == shape and t.get_device() == device.index and t.is_contiguous()):
+        if dtype not in _SCALE_DTYPES:
+            raise TypeError(f"{name}: expected float8_e8m0fnu or float32, got {dtype}")
+        _need(t, name, dtype, shape, device)
+    return _SCALE_DTYPES[dtype]
 
 
 def _ok(t: torch.Tensor, name: str, dtype, shape, device):
     """_need, with one test where everything is in order (small calls are bound by the host)."""
-    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous()):
         _need(t, name, dtype, shape, device)
 
 
@@ -947,12 +949,14 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     e4m3 and e8m0 per 128 columns), "inv_rms" [N] (for add_rmsnorm_backward).
     ``out`` may hold buffers for any of them; out["res"] may be the residual
     itself."""
-    _need_dim(x, "x", 2)
     shape = x.shape
+    if len(shape) != 2:
+        _need_dim(x, "x", 2)
     N, H = shape
     dev = x.device
     bf16 = torch.bfloat16
-    _ok(x, "x", bf16, shape, dev)
+    if not (x.dtype is bf16 and x.is_contiguous()):
+        _ok(x, "x", bf16, shape, dev)
     _ok(weight, "weight", bf16, (H,), dev)
     if not (y or fp8):
         raise ValueError("add_rmsnorm: ask for y, fp8 or both")
@@ -1004,17 +1008,21 @@ def add_rmsnorm_backward(dy: torch.Tensor, res: torch.Tensor, weight: torch.Tens
     them (res = x without a residual); ``dres`` is the gradient that reaches res
     from the rest of the residual stream.  dx is the gradient of x and of the
     residual alike.  ``grads`` may hold the two buffers."""
-    _need_dim(dy, "dy", 2)
-    N, H = dy.shape
+    shape = dy.shape
+    if len(shape) != 2:
+        _need_dim(dy, "dy", 2)
+    N, H = shape
     dev = dy.device
-    _ok(dy, "dy", torch.bfloat16, (N, H), dev)
-    _ok(res, "res", torch.bfloat16, (N, H), dev)
-    _ok(weight, "weight", torch.bfloat16, (H,), dev)
+    bf16 = torch.bfloat16
+    if not (dy.dtype is bf16 and dy.is_contiguous()):
+        _ok(dy, "dy", bf16, shape, dev)
+    _ok(res, "res", bf16, shape, dev)
+    _ok(weight, "weight", bf16, (H,), dev)
     _ok(inv_rms, "inv_rms", torch.float32, (N,), dev)
     if dres is not None:
-        _ok(dres, "dres", torch.bfloat16, (N, H), dev)
+        _ok(dres, "dres", bf16, shape, dev)
     given = grads.get if grads else _nothing
-    r = dict(dx=_given(given("dx"), "dx", dy, (N, H), torch.bfloat16, stream),
+    r = dict(dx=_given(given("dx"), "dx", dy, shape, bf16, stream),
              dweight=_given(given("dweight"), "dweight", dy, (H,), torch.float32, stream))
     if ws is None:
         ws = _new(dy, (add_rmsnorm_backward_workspace_bytes(N, H),), torch.uint8, stream)
@@ -1061,15 +1069,19 @@ def linear_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     """out [M,N] bf16 = a [M,K] . w [N,K]^T + bias [N], a and w e4m3 with
     scales per block of 128 (moe_fp8_linear).  ``err``: int32 [1], collects
     device error bits."""
-    _need_dim(a, "a", 2)
-    _need_dim(w, "w", 2)
-    M, K = a.shape
-    N = w.shape[0]
+    shape, w_shape = a.shape, w.shape
+    if len(shape) != 2 or len(w_shape) != 2:
+        _need_dim(a, "a", 2)
+        _need_dim(w, "w", 2)
+    M, K = shape
+    N = w_shape[0]
     dev = a.device
-    _ok(a, "a", _E4M3, (M, K), dev)
+    if not (a.dtype is _E4M3 and a.is_contiguous()):
+        _ok(a, "a", _E4M3, shape, dev)
     _ok(w, "w", _E4M3, (N, K), dev)
-    sa = _need_scale(a_scale, "a_scale", (M, _blocks(K)), dev)
-    sw = _need_scale(w_scale, "w_scale", (_blocks(N), _blocks(K)), dev)
+    nk = (K + 127) // 128
+    sa = _need_scale(a_scale, "a_scale", (M, nk), dev)
+    sw = _need_scale(w_scale, "w_scale", ((N + 127) // 128, nk), dev)
     if bias is not None:
         _ok(bias, "bias", torch.bfloat16, (N,), dev)
     if err is not None:
