@@ -969,7 +969,9 @@ def main():
     if world != args.gpus:
         raise SystemExit(f"bench.py: --gpus {args.gpus} but {world} ranks were launched (WORLD_SIZE)")
     if args.check_launch:
-        print(json.dumps({"rank": rank, "world": world, "impl": args.impl}), flush=True)
+        # one write: ranks share the launcher's pipe, unbuffered, and print() writes the newline on its own
+        sys.stdout.write(json.dumps({"rank": rank, "world": world, "impl": args.impl}) + "\n")
+        sys.stdout.flush()
         return
     if args.impl == "reference":
         run_reference(args, rank, world)
