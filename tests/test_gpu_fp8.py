@@ -563,3 +563,64 @@ def test_layer_bias_at_any_even_address():
         assert odd[0].data_ptr() % 16 == 2
         assert torch.equal(binding.forward_fp8(x, xs, idx, wt, w1, s1, w2, s2, *odd),
                            binding.forward_fp8(x, xs, idx, wt, w1, s1, w2, s2, b1, b2))
+
+
+_FIRST = """
+import torch
+from mixture_experts_routed_non_b200 import binding
+x = torch.ones((300, 2048), device="cuda").to(torch.bfloat16)
+w = torch.ones((2048,), device="cuda").to(torch.bfloat16)
+m = torch.ones((2048, 520), device="cuda").to(torch.bfloat16)
+off = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    r = binding.add_rmsnorm(x, w, y=False, fp8=True, inv_rms=True)
+    q, s = binding.quantize_weight_fp8(m)
+    few = binding.linear_fp8(r["y8"][:7], r["y8_scale"][:7], q, s)
+    all = binding.linear_fp8(r["y8"], r["y8_scale"], q, s)
+    two = binding.grouped_linear_fp8(r["y8"], r["y8_scale"], off, torch.stack([q.view(torch.uint8)] * 2).view(q.dtype),
+                                     torch.stack([s.view(torch.uint8)] * 2).view(s.dtype))
+    g = binding.add_rmsnorm_backward(x, x, w, r["inv_rms"])
+graph.replay()
+torch.cuda.synchronize()
+for y in (few, all, two):
+    assert bool((y == 2048).all()), y
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_capture_with_two_streams_that_join():
+    a, s, w, t, b = _linear_case(300, 1024, 512, E8, E8, False, 3)
+    a2, s2, w2, t2, _ = _linear_case(300, 512, 264, E8, E8, False, 4)
+    nw = torch.ones((512,), dtype=BF16, device="cuda")
+    y1 = binding.linear_fp8(a, s, w, t)
+    want = binding.add_rmsnorm(y1, nw, y1, fp8=True)
+    want_z = binding.linear_fp8(want["y8"], want["y8_scale"], w2, t2)
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+    out = [torch.zeros_like(y1), torch.zeros_like(y1)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        binding.linear_fp8(a, s, w, t, out=out[0])
+        with torch.cuda.stream(side):
+            binding.linear_fp8(a, s, w, t, out=out[1])
+        main.wait_stream(side)
+        r = binding.add_rmsnorm(out[0], nw, out[1], fp8=True)  # depends on kernels of both streams
+        z = binding.linear_fp8(r["y8"], r["y8_scale"], w2, t2)
+    for _ in range(20):
+        for o in out:
+            o.zero_()
+        z.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(z, want_z) and torch.equal(r["res"], want["res"])
