@@ -624,3 +624,45 @@ def test_capture_with_two_streams_that_join():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(z, want_z) and torch.equal(r["res"], want["res"])
+
+
+@pytest.mark.parametrize("rows,E,K,N", [(8, 128, 128, 9600), (26700, 3, 128, 4096)])
+@pytest.mark.parametrize("scale", [E8, F32])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_more_tiles_than_a_block_lists(rows, E, K, N, scale, gather):
+    counts = [rows + (e % 3) - 1 for e in range(E)]  # over 64 units (tiles) to a block (pair)
+    a, s, off, w, t, b, idx, P = _grouped_case(counts, K, N, gather, scale, scale, False, 12, spare=2)
+    out = torch.full((P, N), 7.0, dtype=BF16, device="cuda")
+    binding.grouped_linear_fp8(a, s, off, w, t, gather=idx, out=out)
+    assert bool((out[P - 2:] == 7).all())
+    ends = off.tolist()
+    for e in sorted({0, 1, E // 2, E - 1}):
+        p = torch.unique(torch.cat([torch.arange(ends[e], min(ends[e] + 40, ends[e + 1])),
+                                    torch.arange(max(ends[e + 1] - 40, ends[e]), ends[e + 1])])).cuda()
+        src = p if idx is None else idx[p].long()
+        av = ref.values(a.view(torch.uint8)[src].view(a.dtype), s.view(torch.uint8)[src].view(s.dtype)
+                        if s.dtype == E8 else s[src])
+        y, tol = ref.product(av, ref.weight_values(w[e], t[e]), None)
+        ref.check(out[p], y, tol, f"expert {e}")
+
+
+@pytest.mark.parametrize("counts", [[5, 9], [40, 33], [700, 300]])
+@pytest.mark.parametrize("K", [384, 400])
+@pytest.mark.parametrize("scale", [E8, F32])
+def test_rows_outside_are_zeros_whatever_the_first_and_last_row_hold(counts, K, scale):
+    a, s, off, w, t, b, idx, P = _grouped_case(counts, K, 264, True, scale, scale, True, 21)
+    rows = a.shape[0]
+    idx[(idx == 0) | (idx == rows - 1)] = 1
+    want = binding.grouped_linear_fp8(a, s, off, w, t, b, gather=idx)
+    for r in (0, rows - 1):  # the rows that stand in for one outside
+        a.view(torch.uint8)[r] = 0x7F
+        if scale == E8:
+            s.view(torch.uint8)[r] = 255
+        else:
+            s[r] = float("nan")
+    bad = torch.arange(0, P, 3, device="cuda")
+    idx[bad] = torch.tensor([-1, rows, 2 ** 31 - 1, -(2 ** 31)], dtype=torch.int32, device="cuda").repeat(P)[:len(bad)]
+    got = binding.grouped_linear_fp8(a, s, off, w, t, b, gather=idx)
+    expert = torch.searchsorted(off[1:].contiguous(), torch.arange(P, device="cuda", dtype=torch.int32), right=True)
+    want[bad] = b[expert[bad]]
+    assert torch.equal(got, want)

@@ -184,3 +184,20 @@ def test_quantize_weight_is_the_definition(E, K, N):
     if E == 1:
         q2, s2 = binding.quantize_weight_fp8(w[0])
         assert q2.shape == (N, K) and torch.equal(q2.view(torch.uint8), q[0].view(torch.uint8))
+
+
+def test_norm_of_values_whose_scale_and_rms_multiply_past_the_range():
+    """1 / rms = 2^62 and a block's scale 2^-86: their quotient is no fp32 number."""
+    g = _gen(9)
+    sign = torch.where(torch.rand((5, 640), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    x = (sign * 2.0 ** -62).to(BF16)
+    w = torch.full((640,), 2.0 ** -78, device="cuda").to(BF16)
+    x[3], x[4] = 1.0, 0.0     # rows as usual beside them; all zeros with eps = 0 is 0/0
+    out = binding.add_rmsnorm(x, w, None, eps=0.0, fp8=True, inv_rms=True)
+    for r in range(4):
+        _check_forward({k: v[r:r + 1] for k, v in out.items()}, x[r:r + 1], None, w, 0.0)
+    assert bool(out["y"][4].isnan().all()) and bool(out["y8"][4].float().isnan().all())
+    w[:] = 1.0                # infinite products beside finite blocks
+    x[0, 3], w[3] = 2.0 ** 100, 2.0 ** 100
+    out = binding.add_rmsnorm(x[:1], w, None, eps=0.0, fp8=True)
+    assert bool(out["y8"][0, 128:].float().isfinite().all())
