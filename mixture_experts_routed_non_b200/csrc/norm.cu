@@ -20,8 +20,8 @@
 // Bound by HBM: one pass, every tensor read or written once.  Every kernel is a
 // programmatic dependent of the launch before it: its blocks come up and set their
 // barriers while that one ends.  Measured back to back (rates of the bytes that have
-// to move): 16384 x 2048 with residual, 8-bit out 44 us (5.4 TB/s; 45 without the early
-// start); 8191 x 7168 with residual, bf16 out 77 us (6.1 TB/s; 79); gradient of 16384
+// to move): 16384 x 2048 with residual, 8-bit out 43 us (5.5 TB/s; 45 without the early
+// start); 8191 x 7168 with residual, bf16 out 76 us (6.2 TB/s; 79); gradient of 16384
 // x 2048 with dres 48 us (5.6 TB/s; 49), its second kernel included.  Without a
 // residual the 8-bit form has half as many bytes to an instruction and is bound by issuing
 // them: 16384 x 2048 29 us (3.5 TB/s; 32 with two products per value and IEEE divisions).
@@ -402,10 +402,15 @@ cudaError_t launch_rows(Kernel kernel, const Args &a, const NormShape &n, int te
 template <bool kResidual>
 cudaError_t launch_forward(const NormArgs &a, int num_sms, cudaStream_t s) {
     const NormShape n = norm_shape(a.H);
-    // Four blocks to an SM stay resident.  With a bf16 y as many bytes are written as read, and
-    // a second wave of blocks, which staggers loads and stores, is faster (16384 x 2048 48 us
-    // against 52, 8191 x 7168 79 against 84); with y8 alone it is slower (46 against 44).
-    const int64_t groups = (a.N + n.R - 1) / n.R, room = (int64_t)num_sms * (a.y ? 8 : 4);
+    // Four blocks to an SM stay resident.  Where a bf16 y is written as well, more waves of blocks,
+    // which stagger loads and stores, are faster on long rows: eight to an SM (16384 x 2048 with
+    // residual 45.9 us against 48.6, 8191 x 7168 76 against 81), or three row groups to a block
+    // where s is written too, rows are many and no wider than 4096 (40000 x 2048 101 against 111,
+    // 16384 x 2048 44.6 against 45.3; 8191 x 7168 79.3 against 76.8).  Not on short rows (50000 x
+    // 256 16.4 against 16.0) nor with y8 alone (8191 x 7168 71.7 against 71.1).
+    const int64_t groups = (a.N + n.R - 1) / n.R, four = 4 * (int64_t)num_sms, thirds = (groups + 2) / 3;
+    const bool more = a.y && a.H >= 1024 && a.H <= 8192;
+    const int64_t room = !more ? four : kResidual && a.H <= 4096 && thirds > 2 * four ? thirds : 2 * four;
     const unsigned grid = (unsigned)(groups < room ? groups : room);
     const int in = kResidual ? 2 : 1;
     if (n.V == 1) return launch_rows(add_rmsnorm_kernel<1, kResidual>, a, n, in, grid, s);
