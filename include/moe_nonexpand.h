@@ -567,7 +567,8 @@ MOE_API int moe_fp8_quantize_weight(const void *w, int32_t E, int32_t K, int32_t
  * bf16.  Each block of 128 along K is summed by the tensor cores and added in
  * fp32 with its two scales; no long sum is held in less.  K a multiple of 16,
  * N of 8; a, w, out 16-byte aligned.  err_word: device uint32 (MOE_DEVERR_*
- * bits are OR-ed in, never cleared) or NULL.  One kernel launch.
+ * bits are OR-ed in, never cleared) or NULL.  Should a wait inside the kernel give
+ * up (MOE_DEVERR_TIMEOUT), the output of the SMs concerned is NaN.  One kernel launch.
  */
 MOE_API int moe_fp8_linear(const void *a, const void *a_scale, int32_t a_scale_dtype, int64_t M, int32_t K,
                            const void *w, const void *w_scale, int32_t w_scale_dtype, int32_t N, const void *bias,
@@ -659,6 +660,16 @@ MOE_API int moe_nonexpand_read_error(const void *ws, moe_stream_t stream, uint32
  */
 MOE_API int moe_nonexpand_selftest_wait_timeout(void *ws, size_t ws_bytes, uint32_t timeout_us,
                                         moe_stream_t stream);
+
+/*
+ * The same for the 8-bit products where CTAs share a unit's K: the hand-over of
+ * partial sums on constants, so that out is 3 everywhere -- [96,128] bf16, two
+ * CTAs to 32 rows (pairs = 0), or [256,256], two CTA pairs to the tile (pairs =
+ * 1).  With lose = 1 one of the two waits for an accumulator that never comes:
+ * err_word gets MOE_DEVERR_TIMEOUT, and out is NaN everywhere.  out: 16-byte aligned device memory; timeout_us as above.
+ */
+MOE_API int moe_fp8_selftest_wait_timeout(int32_t pairs, int32_t lose, void *out, uint32_t *err_word,
+                                          uint32_t timeout_us, moe_stream_t stream);
 
 /* Static string for a MOE_OK / MOE_ERR_* code. */
 MOE_API const char *moe_nonexpand_strerror(int status);

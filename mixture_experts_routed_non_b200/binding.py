@@ -75,6 +75,7 @@ EXPORTED = (
     "moe_fp8_grouped_linear",
     "moe_fp8_forward_workspace_bytes",
     "moe_fp8_forward",
+    "moe_fp8_selftest_wait_timeout",
 )
 
 EP_MAX_RANKS = 32
@@ -222,6 +223,8 @@ def load() -> ctypes.CDLL:
     lib.moe_fp8_forward.restype = ctypes.c_int
     lib.moe_fp8_forward.argtypes = [P, P, i32, R, i32, i32, i32, P, P, i32, P, P, P, i32, P, i32, i32, P,
                                     ctypes.POINTER(MoeMeta), P, sz, P]
+    lib.moe_fp8_selftest_wait_timeout.restype = ctypes.c_int
+    lib.moe_fp8_selftest_wait_timeout.argtypes = [i32, i32, P, P, ctypes.c_uint32, P]
     lib.moe_nonexpand_strerror.restype = ctypes.c_char_p
     lib.moe_nonexpand_strerror.argtypes = [ctypes.c_int]
     _lib = lib
@@ -1177,3 +1180,15 @@ def forward_fp8(x: torch.Tensor, x_scale: torch.Tensor, expert_idx: torch.Tensor
              w1.data_ptr(), w1_scale.data_ptr(), s1, _ptr(b1), w2.data_ptr(), w2_scale.data_ptr(), s2, _ptr(b2),
              ACT_SWIGLU, layout, out.data_ptr(), ctypes.byref(m) if m is not None else None, ws.data_ptr(), ws.numel())
     return out
+
+
+def selftest_fp8_wait_timeout(pairs: bool, lose: bool, timeout_us: int, device="cuda",
+                              stream: Optional[torch.cuda.Stream] = None):
+    """The 8-bit products' hand-over of partial sums on constants (moe_fp8_selftest_wait_timeout):
+    (out, err), out [96,128] bf16 or, with ``pairs``, [256,256].  ``lose``: with an accumulator that
+    never comes."""
+    err = torch.zeros(1, dtype=torch.int32, device=device)
+    out = torch.zeros((256, 256) if pairs else (96, 128), dtype=torch.bfloat16, device=device)
+    _call_on(out.device, stream, "moe_fp8_selftest_wait_timeout", int(pairs), int(lose), out.data_ptr(), err.data_ptr(),
+             timeout_us)
+    return out, err

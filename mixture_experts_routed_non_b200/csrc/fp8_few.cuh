@@ -138,14 +138,15 @@ __device__ __forceinline__ void gather_chunk_rows(const Fp8GemmArgs &a, const FU
 
 // Hands this warp's partial sums over and waits for everybody's.
 __device__ __forceinline__ void partials_ready(uint32_t rfull_bar, uint32_t parity, int S, int lane,
-                                               volatile uint32_t *abort) {
+                                               volatile uint32_t *abort,
+                                               unsigned long long timeout_ns = kWaitTimeoutNs) {
     __syncwarp();
     if (S == 1) {
         if (lane == 0) mbar_arrive(rfull_bar);
     } else if (lane < S) {
         mbar_arrive_cluster_release(mapa_shared(rfull_bar, lane));
     }
-    mbar_wait_bounded(rfull_bar, parity, abort);
+    epi_wait(rfull_bar, parity, abort, S, timeout_ns);
     if (S > 1) fence_acquire_cluster();
     __syncwarp();
 }
@@ -180,7 +181,7 @@ struct FGone {
 // the S CTAs.
 template <int CN, int kMode, bool kGather>
 __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q, int rank, int S, int tid, bool concat,
-                                           uint32_t red, const uint8_t *red_ptr, const FGone<CN> &gone, bool ok) {
+                                           uint32_t red, const uint8_t *red_ptr, const FGone<CN> &gone) {
     constexpr int kAcc = kMode == kFp8SwiGlu ? 2 : 1;
     // Tokens rank, rank + S, ...: eight at a time, 16 threads each, eight neighbouring
     // columns per thread.
@@ -224,7 +225,7 @@ __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q,
             keep(v);
             if (n < a.N) bias8(n, v);
             if (kMode == kFp8Bf16) {
-                if (ok && has && n < a.N)
+                if (has && n < a.N)
                     *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + p * a.N + n) =
                         make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                    pack_bf16x2(v[6], v[7]));
@@ -236,7 +237,7 @@ __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q,
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 const int ex = y_block_exp(m);
                 const float sc = exp2i(-ex);
-                if (ok && has) {
+                if (has) {
                     *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + p * a.N + n) =
                         make_uint4(pack_f16x2(v[0] * sc, v[1] * sc), pack_f16x2(v[2] * sc, v[3] * sc),
                                    pack_f16x2(v[4] * sc, v[5] * sc), pack_f16x2(v[6] * sc, v[7] * sc));
@@ -281,13 +282,29 @@ __device__ __forceinline__ void few_output(const Fp8GemmArgs &a, const FUnit &q,
             for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const uint32_t e = e4m3_scale_exp(m);
             const float is = inv_scale_of_exp(e);
-            if (ok && has) {
+            if (has) {
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + p * (a.N / 2) + q.nt * 128 + c8) =
                     make_uint2(pack_e4m3x4(g[0] * is, g[1] * is, g[2] * is, g[3] * is),
                                pack_e4m3x4(g[4] * is, g[5] * is, g[6] * is, g[7] * is));
                 if ((tid & 15) == 0)
                     static_cast<uint8_t *>(a.out_scale)[p * (a.N / 256) + q.nt] = (uint8_t)e;
             }
+        }
+    }
+}
+
+// nan_tiles for the few-row kernels: the tokens of this CTA in all of its units.
+template <int CN, int kMode, bool kOne>
+__device__ __forceinline__ void nan_units(const Fp8GemmArgs &a, const FUnits<CN, kMode, kOne> &list, int units, int u0, int du,
+                                          int rank, int S, int tid) {
+    for (int u = u0, n = 0; u < units; u += du, ++n) {
+        const FUnit q = list.at(u, n);
+        const int col = q.nt * kFM + (tid & 15) * 8;  // (of h, with SwiGLU)
+        if (col >= (kMode == kFp8SwiGlu ? a.N / 2 : a.N)) continue;
+        for (int j = rank + (tid >> 4) * S; j < q.nv; j += 8 * S) {
+            const size_t p = (size_t)q.m0 + j;
+            store_nan<kMode>(static_cast<uint8_t *>(a.out) + (kMode == kFp8SwiGlu ? p * (a.N / 2) + col : 2 * (p * a.N + col)),
+                             kMode == kFp8SwiGlu ? 8 : 16);
         }
     }
 }

@@ -14,7 +14,7 @@
 // the rows or gather relay, 3 idle, 4-7 = scales (one per TMEM lane quarter), 8-11 =
 // epilogue, 12-13 = row gather (gathered rows only).  Every wait is bounded
 // (common.cuh); one that gives up raises the CTA's abort flag, on which every role
-// runs out without storing, and the error word gets MOE_DEVERR_TIMEOUT.
+// runs out, the cluster's output becomes NaN, and the error word gets MOE_DEVERR_TIMEOUT.
 #include "fp8_few.cuh"
 #include "fp8_mx.cuh"
 
@@ -344,9 +344,9 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
             const uint32_t b = it & 1u;
             FGone<CN> gone;
             if (kGather) gone.load(a, q, lane);
-            mbar_wait_bounded(tfull_bar(b), (it >> 1) & 1u, abort);
+            epi_wait(tfull_bar(b), (it >> 1) & 1u, abort, S);
             // the partial sums of the unit before have been read, here and by the peers
-            mbar_wait_bounded(rempty_bar, (it & 1u) ^ 1u, abort);
+            epi_wait(rempty_bar, (it & 1u) ^ 1u, abort, S);
             __syncwarp();
             if (kGather) gone.look(a);
             tc_fence_after();
@@ -366,8 +366,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty_bar(b));
             partials_ready(rfull_bar, it & 1u, S, lane, abort);
-            const bool ok = *abort == 0;
-            few_output<CN, kMode, kGather>(a, q, rank, S, tid, concat, red, base_ptr + C::kRedOff, gone, ok);
+            few_output<CN, kMode, kGather>(a, q, rank, S, tid, concat, red, base_ptr + C::kRedOff, gone);
             partials_read(rempty_bar, S, lane);
         }
     } else if (kGather && warp >= 12) {
@@ -392,6 +391,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
         tc_fence_after();
         tmem_dealloc(tmem_base, C::kTmem);
     }
+    if (*abort && warp >= 8 && warp < 12) nan_units(a, list, units, u0, du, rank, S, (int)threadIdx.x - 256);
 }
 
 template <int CN, int kMode, bool kGather, bool kOne>

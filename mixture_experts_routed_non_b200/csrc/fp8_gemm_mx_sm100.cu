@@ -371,10 +371,10 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(x_threads(k
         const uint32_t tb = tmem_base + ((uint32_t)(32 * q4) << 16);
         uint32_t tphase = 0;
         // a wait that gives up raises the abort flag; the warp then runs on over whatever is there
-        // (later waits give up at once), meets the named barriers, and stores nothing
+        // (later waits give up at once) and meets the barriers; NaN is written at the end
         for (int u = t0, i = 0; u < tiles; u += dt, ++i, tphase ^= 1u) {
             const PTile t = list.at(u, i);
-            mbar_wait_bounded(tfull_bar, tphase, abort);
+            epi_wait(tfull_bar, tphase, abort, 2 * kSplit);
             __syncwarp();
             tc_fence_after();
             uint32_t v0[32], v1[32];
@@ -391,8 +391,7 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(x_threads(k
                 acc[32 + j] = __uint_as_float(v1[j]);
             }
             if (kSplit > 1 && !pair_share<kSplit>(acc, base, (int)rank, pi, cq, q4, lane)) continue;
-            pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s + (i & 1) * 512,
-                                        *abort == 0);
+            pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s + (i & 1) * 512);
         }
         if (lane == 0) bulk_wait0();  // this warp's stores are complete
     } else {
@@ -420,6 +419,7 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(x_threads(k
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, kPTmem);
     }
+    if (*abort && warp >= 8 && warp < 24) nan_tiles<kMode>(a, list, tiles, t0, dt, (int)rank, (warp - 8) >> 2, warp & 3, lane);
 }
 
 template <int kMode, bool kGather, bool kOne, int kSplit>

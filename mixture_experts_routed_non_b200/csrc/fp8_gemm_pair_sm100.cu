@@ -375,14 +375,14 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(p_threads(k
         uint32_t it = 0, sphase = 0;
         int slot = 0;
         // a wait that gives up raises the abort flag; the warp then runs on over whatever is there
-        // (later waits give up at once), meets the named barriers, and stores nothing
+        // (later waits give up at once) and meets the barriers; NaN is written at the end
         for (int u = t0, i = 0; u < tiles; u += dt, ++i) {
             const PTile t = list.at(u, i);
             float acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0.f;
             for (int kb = kb0; kb < kb1; kb += 4) {
-                mbar_wait_bounded(sfull_bar(slot), sphase, abort);
+                epi_wait(sfull_bar(slot), sphase, abort, 2 * kSplit);
                 __syncwarp();
                 float f0[4], f1[4];
 #pragma unroll
@@ -394,7 +394,7 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(p_threads(k
                 for (int k = 0; k < 4; ++k) {
                     if (kb + k < kb1) {
                         const uint32_t b = it & 1u;
-                        mbar_wait_bounded(tfull_bar(b), (it >> 1) & 1u, abort);
+                        epi_wait(tfull_bar(b), (it >> 1) & 1u, abort, 2 * kSplit);
                         ++it;
                         __syncwarp();
                         tc_fence_after();
@@ -426,8 +426,7 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(p_threads(k
                 }
             }
             if (kSplit > 1 && !pair_share<kSplit>(acc, base, (int)rank, pi, cq, q4, lane)) continue;
-            pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s + (i & 1) * 512,
-                                        *abort == 0);
+            pair_output<kMode, kGather>(a, t, acc, (int)rank, cq, q4, lane, concat, buf, max_s + (i & 1) * 512);
         }
         if (lane == 0) bulk_wait0();  // this warp's stores are complete
     } else {
@@ -455,6 +454,7 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(p_threads(k
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, kPTmem);
     }
+    if (*abort && warp >= 4 && warp < 20) nan_tiles<kMode>(a, list, tiles, t0, dt, (int)rank, (warp - 4) >> 2, warp & 3, lane);
 }
 
 template <int kMode, bool kGather, bool kOne, int kSplit>

@@ -20,8 +20,8 @@
 // Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer, 2 = TMA of
 // the rows or gather relay, 3 idle, 4-7 = epilogue (TMEM lane quarter warp%4), 8-9 =
 // row gather (gathered rows only).  Every wait is bounded (common.cuh); one that gives
-// up raises the CTA's abort flag, on which every role runs out without storing, and
-// the error word gets MOE_DEVERR_TIMEOUT.
+// up raises the CTA's abort flag, on which every role runs out, the cluster's output
+// becomes NaN, and the error word gets MOE_DEVERR_TIMEOUT.
 #include "fp8_few.cuh"
 
 namespace moe {
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
         const uint32_t red = base + (uint32_t)C::kRedOff;
         float *red_s = reinterpret_cast<float *>(base_ptr + C::kRedOff);
         uint32_t it = 0, uc = 0;
-        // after a wait that gave up the warps run on over whatever is there, meet the named
-        // barriers and store nothing
+        // after a wait that gave up the warps run on over whatever is there and meet the
+        // barriers; NaN is written at the end
         for (int u = u0, n = 0; u < units; u += du, ++n, ++uc) {
             const FUnit q = list.at(u, n);
             FGone<CN> gone;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
                 }
                 if (kb + 1 < kb1) load_block(kb + 1);
                 q_epilogue_bar();  // this block's scales are in; the other buffer's have all been read
-                mbar_wait_bounded(tfull_bar(b), (it >> 1) & 1u, abort);
+                epi_wait(tfull_bar(b), (it >> 1) & 1u, abort, S);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
                 }
             }
             // the partial sums of the unit before have been read, here and by the peers
-            mbar_wait_bounded(rempty_bar, (uc & 1u) ^ 1u, abort);
+            epi_wait(rempty_bar, (uc & 1u) ^ 1u, abort, S);
             __syncwarp();
             if (kGather) gone.look(a);
 #pragma unroll
@@ -290,8 +290,7 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
 #pragma unroll
                 for (int j = 0; j < CN; ++j) red_s[(t * CN + j) * kFM + 32 * q4 + lane] = acc[t][j];
             partials_ready(rfull_bar, uc & 1u, S, lane, abort);
-            few_output<CN, kMode, kGather>(a, q, rank, S, tid, concat, red, base_ptr + C::kRedOff, gone,
-                                           *abort == 0);
+            few_output<CN, kMode, kGather>(a, q, rank, S, tid, concat, red, base_ptr + C::kRedOff, gone);
             partials_read(rempty_bar, S, lane);
         }
     } else if (kGather && warp >= 8) {
@@ -316,6 +315,7 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
         tc_fence_after();
         tmem_dealloc(tmem_base, C::kTmem);
     }
+    if (*abort && warp >= 4 && warp < 8) nan_units(a, list, units, u0, du, rank, S, (int)threadIdx.x - 128);
 }
 
 template <int kMode, bool kGather, bool kOne>

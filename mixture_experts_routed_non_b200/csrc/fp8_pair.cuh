@@ -39,6 +39,23 @@ __device__ __forceinline__ void regs_dec() {
 // The four epilogue warps that share a lane quarter's rows.
 __device__ __forceinline__ void p_rows_bar(int q4) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q4) : "memory"); }
 
+// The flag (a shared address) in all CTAs of the cluster.  (Kept out of the warps' code: inlined it cost
+// layers of 8 and 512 tokens 4 and 2 %.)
+static __device__ __noinline__ void raise_abort(uint32_t flag, int ctas) {
+    for (int c = 0; c < ctas && ctas > 1; ++c)  // (its own is up)
+        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa_shared(flag, (uint32_t)c)), "r"(1u) : "memory");
+}
+// A wait of an epilogue warp.  Where it gives up, the abort flag goes up in all CTAs of the cluster; the
+// warp runs on over whatever is there and meets the barriers.  What it writes or lets others write from
+// then on may be wrong, in the peers as well.  So every CTA looks at its flag once the whole cluster is
+// through, and writes NaN over its output where it is up.  (Nothing is added where a wait succeeds: a note
+// of each wait's result, or a vote on it, cost 3-6 % of the products with fp32 scales, a third of 1001 x
+// 2000 x 1496.)
+__device__ __forceinline__ void epi_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort, int ctas,
+                                         unsigned long long timeout_ns = kWaitTimeoutNs) {
+    if (!mbar_wait_bounded(bar, parity, abort, timeout_ns)) raise_abort(smem_u32(const_cast<const uint32_t *>(abort)), ctas);
+}
+
 // Four floats of another CTA's shared memory.
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
     float4 v;
@@ -277,11 +294,11 @@ __device__ __forceinline__ bool bias_aligned(const Fp8GemmArgs &a) {
 // barrier these have been read.  All 16 warps call it.
 template <int kMode, bool kGather>
 __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t, float (&acc)[64], int rank, int cq,
-                                            int q4, int lane, bool concat, uint32_t buf, float *max_s, bool ok) {
+                                            int q4, int lane, bool concat, uint32_t buf, float *max_s) {
     const int r = 32 * q4 + lane;
     const int row0 = t.m0 + rank * 128 + q4 * 32;
     const int p = row0 + lane;
-    const bool store = ok && p < t.m_end;
+    const bool store = p < t.m_end;
     if (kGather && p < t.m_end) {  // a gathered row outside `a` counts as zeros
         const int src = __ldg(a.gather + p);
         if (src < 0 || src >= a.rows) {
@@ -324,7 +341,7 @@ __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t
                     v[j] = kMode == kFp8Y16 ? pack_f16x2(acc[32 * i + 2 * j], acc[32 * i + 2 * j + 1])
                                             : pack_bf16x2(acc[32 * i + 2 * j], acc[32 * i + 2 * j + 1]);
                 if (col + 32 * i < a.N)
-                    store32(&a.tmap_out, buf, lane, ok && row0 + 31 < t.m_end, store, row0,
+                    store32(&a.tmap_out, buf, lane, row0 + 31 < t.m_end, store, row0,
                             static_cast<uint16_t *>(a.out) + (size_t)(store ? p : 0) * a.N, col + 32 * i, a.N, v);
             }
         }
@@ -367,6 +384,27 @@ __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t
             }
             if (cq == 0) static_cast<uint8_t *>(a.out_scale)[(size_t)p * (a.N / 256) + t.nt] = (uint8_t)e;
         }
+    }
+}
+
+// NaN into `bytes` bytes of output (a multiple of 8, aligned to it): all ones but the signs, in each of the types.
+template <int kMode>
+__device__ __forceinline__ void store_nan(uint8_t *out, int bytes) {
+    const uint32_t v = kMode == kFp8SwiGlu ? 0x7F7F7F7Fu : 0x7FFF7FFFu;
+    for (int i = 0; i < bytes; i += 8) *reinterpret_cast<uint2 *>(out + i) = make_uint2(v, v);
+}
+// NaN over an epilogue warp's part of all of the cluster's tiles (epi_wait).
+template <int kMode, bool kOne>
+__device__ __forceinline__ void nan_tiles(const Fp8GemmArgs &a, const PTiles<kOne> &list, int tiles, int t0, int dt, int rank,
+                                          int cq, int q4, int lane) {
+    for (int u = t0, i = 0; u < tiles; u += dt, ++i) {
+        const PTile t = list.at(u, i);
+        const int p = t.m0 + rank * 128 + q4 * 32 + lane;
+        const int col = kMode == kFp8SwiGlu ? t.nt * 128 + cq * 32 : t.nt * kPN + cq * 64;
+        const int row_bytes = kMode == kFp8SwiGlu ? a.N / 2 : 2 * a.N, size = kMode == kFp8SwiGlu ? 1 : 2;
+        if (p < t.m_end)
+            store_nan<kMode>(static_cast<uint8_t *>(a.out) + (size_t)p * row_bytes + (size_t)col * size,
+                             min(kMode == kFp8SwiGlu ? 32 : 128, row_bytes - col * size));
     }
 }
 
