@@ -526,7 +526,9 @@ MOE_API int moe_ep_combine(const moe_ep_sources_t *src, const int32_t *send_idx,
  * fp32 or NULL (the backward reads it).  res may be residual or x itself, and
  * y may be x; no other buffers may overlap.  Sums are fp32; y is rounded once
  * to each output type.  H a multiple of 8, at most 16384; eps >= 0; bf16 and
- * e4m3 buffers 16-byte aligned.  One kernel launch.
+ * e4m3 buffers 16-byte aligned.  Should a wait inside the kernel give up, the
+ * block's rows from there on are NaN in every output, res among them.  One kernel
+ * launch.
  */
 MOE_API int moe_add_rmsnorm(const void *x, const void *residual, const void *weight, int64_t N, int32_t H, float eps,
                             void *res, void *y, void *y8, void *y8_scale, float *inv_rms, moe_stream_t stream);
@@ -670,6 +672,15 @@ MOE_API int moe_nonexpand_selftest_wait_timeout(void *ws, size_t ws_bytes, uint3
  */
 MOE_API int moe_fp8_selftest_wait_timeout(int32_t pairs, int32_t lose, void *out, uint32_t *err_word,
                                           uint32_t timeout_us, moe_stream_t stream);
+
+/*
+ * And for the norm with a residual (H at most 256): one block takes all N rows,
+ * and from its third turn on (32 rows of up to 128 columns, 16 of more) the loads
+ * never come.  Those rows are NaN in res, y and inv_rms.
+ */
+MOE_API int moe_add_rmsnorm_selftest_wait_timeout(const void *x, const void *residual, const void *weight, int64_t N,
+                                                  int32_t H, float eps, void *res, void *y, float *inv_rms,
+                                                  moe_stream_t stream);
 
 /* Static string for a MOE_OK / MOE_ERR_* code. */
 MOE_API const char *moe_nonexpand_strerror(int status);

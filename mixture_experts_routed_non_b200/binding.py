@@ -76,6 +76,7 @@ EXPORTED = (
     "moe_fp8_forward_workspace_bytes",
     "moe_fp8_forward",
     "moe_fp8_selftest_wait_timeout",
+    "moe_add_rmsnorm_selftest_wait_timeout",
 )
 
 EP_MAX_RANKS = 32
@@ -225,6 +226,8 @@ def load() -> ctypes.CDLL:
                                     ctypes.POINTER(MoeMeta), P, sz, P]
     lib.moe_fp8_selftest_wait_timeout.restype = ctypes.c_int
     lib.moe_fp8_selftest_wait_timeout.argtypes = [i32, i32, P, P, ctypes.c_uint32, P]
+    lib.moe_add_rmsnorm_selftest_wait_timeout.restype = ctypes.c_int
+    lib.moe_add_rmsnorm_selftest_wait_timeout.argtypes = [P, P, P, i64, i32, f32, P, P, P, P]
     lib.moe_nonexpand_strerror.restype = ctypes.c_char_p
     lib.moe_nonexpand_strerror.argtypes = [ctypes.c_int]
     _lib = lib
@@ -1192,3 +1195,16 @@ def selftest_fp8_wait_timeout(pairs: bool, lose: bool, timeout_us: int, device="
     _call_on(out.device, stream, "moe_fp8_selftest_wait_timeout", int(pairs), int(lose), out.data_ptr(), err.data_ptr(),
              timeout_us)
     return out, err
+
+
+def selftest_rmsnorm_wait_timeout(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor, *, eps: float = 1e-6,
+                                  stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """add_rmsnorm(x, weight, residual, inv_rms=True), with res over the residual, whose loads from a
+    block's third turn on never come (moe_add_rmsnorm_selftest_wait_timeout)."""
+    N, H = x.shape
+    for t, name, shape in ((x, "x", (N, H)), (weight, "weight", (H,)), (residual, "residual", (N, H))):
+        _ok(t, name, torch.bfloat16, shape, x.device)
+    r = dict(res=residual, y=_new(x, (N, H), torch.bfloat16, stream), inv_rms=_new(x, (N,), torch.float32, stream))
+    _call_on(x.device, stream, "moe_add_rmsnorm_selftest_wait_timeout", x.data_ptr(), residual.data_ptr(), weight.data_ptr(),
+             N, H, eps, residual.data_ptr(), r["y"].data_ptr(), r["inv_rms"].data_ptr())
+    return r

@@ -68,6 +68,7 @@ struct NormArgs {
     float eps;
 };
 cudaError_t launch_add_rmsnorm(const NormArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_add_rmsnorm_selftest(const NormArgs &a, cudaStream_t s);  // H <= 256, with a residual
 
 struct NormBwdArgs {
     const __nv_bfloat16 *dy, *res, *weight, *dres;

@@ -57,11 +57,9 @@ int product(const void *a, const void *a_scale, int32_t a_sd, int64_t rows, int3
                                                                                                       : MOE_ERR_CUDA;
 }
 
-}  // namespace
-
-extern "C" MOE_API int moe_add_rmsnorm(const void *x, const void *residual, const void *weight, int64_t N, int32_t H,
-                                       float eps, void *res, void *y, void *y8, void *y8_scale, float *inv_rms,
-                                       moe_stream_t stream) {
+// The norm's arguments checked (the device last) and put together.
+int norm_args(const void *x, const void *residual, const void *weight, int64_t N, int32_t H, float eps, void *res,
+              void *y, void *y8, void *y8_scale, float *inv_rms, NormArgs *a, int *sms) {
     if (N < 0 || N >= kMaxRows || !(eps >= 0.f)) return MOE_ERR_ARG;
     if (H < 8 || H % 8 != 0 || H > kMaxNormH) return MOE_ERR_SHAPE;
     if (!weight) return MOE_ERR_ARG;
@@ -70,22 +68,44 @@ extern "C" MOE_API int moe_add_rmsnorm(const void *x, const void *residual, cons
     if (!ptr_aligned(x, 16) || !ptr_aligned(residual, 16) || !ptr_aligned(weight, 16) || !ptr_aligned(res, 16) ||
         !ptr_aligned(y, 16) || !ptr_aligned(y8, 16) || !ptr_aligned(inv_rms, 4))
         return MOE_ERR_ARG;
-    int sms = 0;
-    const int st = current_device_sms(&sms);
+    const int st = current_device_sms(sms);
     if (st) return st;
+    a->x = static_cast<const __nv_bfloat16 *>(x);
+    a->residual = static_cast<const __nv_bfloat16 *>(residual);
+    a->weight = static_cast<const __nv_bfloat16 *>(weight);
+    a->res = static_cast<__nv_bfloat16 *>(res);
+    a->y = static_cast<__nv_bfloat16 *>(y);
+    a->y8 = static_cast<uint8_t *>(y8);
+    a->y8_scale = static_cast<uint8_t *>(y8_scale);
+    a->inv_rms = inv_rms;
+    a->N = N;
+    a->H = H;
+    a->eps = eps;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" MOE_API int moe_add_rmsnorm(const void *x, const void *residual, const void *weight, int64_t N, int32_t H,
+                                       float eps, void *res, void *y, void *y8, void *y8_scale, float *inv_rms,
+                                       moe_stream_t stream) {
     NormArgs a;
-    a.x = static_cast<const __nv_bfloat16 *>(x);
-    a.residual = static_cast<const __nv_bfloat16 *>(residual);
-    a.weight = static_cast<const __nv_bfloat16 *>(weight);
-    a.res = static_cast<__nv_bfloat16 *>(res);
-    a.y = static_cast<__nv_bfloat16 *>(y);
-    a.y8 = static_cast<uint8_t *>(y8);
-    a.y8_scale = static_cast<uint8_t *>(y8_scale);
-    a.inv_rms = inv_rms;
-    a.N = N;
-    a.H = H;
-    a.eps = eps;
+    int sms = 0;
+    const int st = norm_args(x, residual, weight, N, H, eps, res, y, y8, y8_scale, inv_rms, &a, &sms);
+    if (st) return st;
     return launch_add_rmsnorm(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" MOE_API int moe_add_rmsnorm_selftest_wait_timeout(const void *x, const void *residual, const void *weight,
+                                                             int64_t N, int32_t H, float eps, void *res, void *y,
+                                                             float *inv_rms, moe_stream_t stream) {
+    if (N < 1 || !residual || !y) return MOE_ERR_ARG;
+    if (H > 256) return MOE_ERR_SHAPE;
+    NormArgs a;
+    int sms = 0;
+    const int st = norm_args(x, residual, weight, N, H, eps, res, y, nullptr, nullptr, inv_rms, &a, &sms);
+    if (st) return st;
+    return launch_add_rmsnorm_selftest(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" MOE_API size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t N, int32_t H) {

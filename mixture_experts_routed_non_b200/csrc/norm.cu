@@ -63,7 +63,8 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 // of kIn tensors (whole rows are contiguous: one bulk copy per tensor), loaded ahead
 // by thread (0, 0).  What the loads need in flight -- several times what two loads per
 // thread can hold -- then costs shared memory instead of registers.
-template <int kIn>
+// kLose (self-test): the loads from the block's third turn on never come, and waits give up after 20 ms.
+template <int kIn, bool kLose = false>
 struct RowRing {
     const __nv_bfloat16 *src[kIn];
     uint32_t bars, data;  // shared addresses: a barrier per stage, the stages
@@ -96,6 +97,7 @@ struct RowRing {
     // thread (0, 0): load the block's rows from row0 on into a stage that nobody reads any more
     __device__ __forceinline__ void fetch(int stage, int64_t row0) const {
         if (row0 >= N || *(volatile uint32_t *)gave_up) return;
+        if (kLose && row0 >= 2 * step) return;
         const int64_t left = N - row0;
         const uint32_t bytes = row_bytes * (uint32_t)(left < blockDim.y ? left : blockDim.y);
         mbar_arrive_expect_tx(bars + 8 * stage, kIn * bytes);
@@ -108,7 +110,7 @@ struct RowRing {
                          : "memory");
     }
     __device__ __forceinline__ void wait(int stage, uint32_t phase) const {
-        mbar_wait_bounded(bars + 8 * stage, phase, gave_up);
+        mbar_wait_bounded(bars + 8 * stage, phase, gave_up, kLose ? 20000000ull : kWaitTimeoutNs);
     }
     // behind the last row; after a wait that gave up: time for copies in flight to land
     __device__ __forceinline__ void end() const {
@@ -127,9 +129,15 @@ struct RowRing {
     }
 };
 
+// This thread's chunks of a row: NaN.
+__device__ __noinline__ void nan_row(__nv_bfloat16 *row, int chunks) {
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x)
+        *reinterpret_cast<uint4 *>(row + c * 8) = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
 // Thread (x, y) of a block works on row y of the block's rows, on the 8-column
 // chunks x, x + T, ... (V of them); a block takes rows until there are none.
-template <int V, bool kResidual>
+template <int V, bool kResidual, bool kLose = false>
 __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a) {
     extern __shared__ __align__(128) uint8_t ring_smem[];
     __shared__ float red[2][kNMaxT / 32];
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
     const int blocks = (a.H + kScaleBlock - 1) / kScaleBlock;
     float *my_red[2] = {red[0] + threadIdx.y * (T / 32), red[1] + threadIdx.y * (T / 32)};
     int64_t row0 = (int64_t)blockIdx.x * blockDim.y;  // of the block: every thread makes the same turns
-    RowRing<kResidual ? 2 : 1> ring;
+    RowRing<kResidual ? 2 : 1, kLose> ring;
     ring.src[0] = a.x;
     if (kResidual) ring.src[kResidual ? 1 : 0] = a.residual;
     ring.start(smem_u32(ring_smem), a.H, a.N, row0, &gave_up);
@@ -151,6 +159,7 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
     }
     int stage = 0;
     uint32_t phase = 0;
+    int64_t lost = -1;  // this thread's first row whose load did not come
     for (int b = 0; row0 < a.N; row0 += ring.step, b ^= 1) {
         const int64_t row = row0 + threadIdx.y;
         const size_t at0 = (size_t)row * a.H;
@@ -183,7 +192,10 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
             phase ^= 1u;
         }
         float inv = rsqrtf(fmaf(ss, per_h, a.eps));  // (within 2 units in the last place)
-        if (*(volatile uint32_t *)&gave_up) inv = __uint_as_float(0x7FC00000u);  // a load never came: NaN, not a wrong value
+        if (*(volatile uint32_t *)&gave_up) {  // a load never came: NaN, not a wrong value
+            inv = __uint_as_float(0x7FC00000u);
+            if (lost < 0) lost = row;
+        }
         if (a.inv_rms && threadIdx.x == 0 && row < a.N) a.inv_rms[row] = inv;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -235,6 +247,9 @@ __global__ void __launch_bounds__(kNMaxT, 2) add_rmsnorm_kernel(const NormArgs a
         }
     }
     ring.end();
+    // s has been written from whatever was there (at the row itself this cost a single row 0.1 us)
+    if (kResidual && lost >= 0)
+        for (; lost < a.N; lost += ring.step) nan_row(a.res + (size_t)lost * a.H, chunks);
 }
 
 // The same walk over the rows; each block sums its rows' dw in registers, adds up
@@ -428,6 +443,10 @@ cudaError_t launch_backward(const NormBwdArgs &a, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_add_rmsnorm_selftest(const NormArgs &a, cudaStream_t s) {
+    return launch_rows(add_rmsnorm_kernel<1, true, true>, a, norm_shape(a.H), 2, 1, s);
+}
 
 int norm_bwd_parts(int64_t N, int H) {
     const int64_t groups = (N + norm_shape(H).R - 1) / norm_shape(H).R;
