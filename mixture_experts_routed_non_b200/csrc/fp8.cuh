@@ -110,6 +110,22 @@ __device__ __forceinline__ uint32_t e4m3_scale_exp(float amax) {
 __device__ __forceinline__ float scale_of_exp(uint32_t e) { return __uint_as_float(e << 23); }          // 1..254
 __device__ __forceinline__ float inv_scale_of_exp(uint32_t e) { return __uint_as_float((254u - e) << 23); }  // 1..253
 
+// A load of what a launch before may have written: it stays behind the wait for that launch, which this
+// one overlaps (pdl_wait).  The read-only loads (__ldg) take memory that nobody writes while the kernel
+// runs, and the compiler may move them ahead of the wait.  Nothing waits for it here.
+template <typename T>
+__device__ __forceinline__ T load_now(const T *p) {
+    static_assert(sizeof(T) == 4, "a 32-bit word");
+    T v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_now(const uint8_t *p) {
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
 // A scale in two steps, for loads that should be in flight together: the raw bits of
 // n scales (e8m0 bytes or fp32) from index i on (behind `last` more, the last one
 // repeated), and their values (e8m0: 0 is 2^-127, 255 is NaN).
@@ -117,10 +133,10 @@ template <int n>
 __device__ __forceinline__ void load_scale_bits(const void *p, int f32, size_t i, int last, uint32_t (&raw)[n]) {
     if (f32) {
 #pragma unroll
-        for (int k = 0; k < n; ++k) raw[k] = __ldg(static_cast<const uint32_t *>(p) + i + min(k, last));
+        for (int k = 0; k < n; ++k) raw[k] = load_now(static_cast<const uint32_t *>(p) + i + min(k, last));
     } else {
 #pragma unroll
-        for (int k = 0; k < n; ++k) raw[k] = __ldg(static_cast<const uint8_t *>(p) + i + min(k, last));
+        for (int k = 0; k < n; ++k) raw[k] = load_now(static_cast<const uint8_t *>(p) + i + min(k, last));
     }
 }
 __device__ __forceinline__ float scale_of_bits(uint32_t raw, int f32) {

@@ -115,7 +115,7 @@ __device__ __forceinline__ void gather_chunk_rows(const Fp8GemmArgs &a, const FU
         int row[CN / 8];  // -1: not copied
 #pragma unroll
         for (int i = 0; i < CN / 8; ++i)
-            row[i] = r0 + 8 * i < q.nv ? (int)min((long long)max(__ldg(a.gather + q.m0 + r0 + 8 * i), 0),
+            row[i] = r0 + 8 * i < q.nv ? (int)min((long long)max(load_now(a.gather + q.m0 + r0 + 8 * i), 0),
                                                   (long long)a.rows - 1)
                                        : -1;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -168,7 +168,7 @@ struct FGone {
     uint32_t bits[CN / 32];
     __device__ __forceinline__ void load(const Fp8GemmArgs &a, const FUnit &q, int lane) {
 #pragma unroll
-        for (int i = 0; i < CN / 32; ++i) src[i] = 32 * i + lane < q.nv ? __ldg(a.gather + q.m0 + 32 * i + lane) : 0;
+        for (int i = 0; i < CN / 32; ++i) src[i] = 32 * i + lane < q.nv ? load_now(a.gather + q.m0 + 32 * i + lane) : 0;
     }
     __device__ __forceinline__ void look(const Fp8GemmArgs &a) {
 #pragma unroll

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kGather ? 448 : 384, 1) fp8_few_kernel(const _
 #pragma unroll
             for (int i = 0; i < kR; ++i) {
                 const int j = 32 * i + lane;
-                nrow[i] = u < units && j < q.nv ? (kGather ? __ldg(a.gather + q.m0 + j) : q.m0 + j) : -1;
+                nrow[i] = u < units && j < q.nv ? (kGather ? load_now(a.gather + q.m0 + j) : q.m0 + j) : -1;
             }
         };
         auto enter_unit = [&]() {  // the unit load_rows has just been called for

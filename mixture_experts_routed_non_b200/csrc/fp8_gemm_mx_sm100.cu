@@ -302,7 +302,7 @@ __global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(x_threads(k
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int p = t.m0 + (int)rank * 128 + 32 * i + lane;
-                nrow[i] = u < tiles && p < t.m_end ? (kGather ? __ldg(a.gather + p) : p) : -1;
+                nrow[i] = u < tiles && p < t.m_end ? (kGather ? load_now(a.gather + p) : p) : -1;
             }
         };
         auto enter_tile = [&]() {  // the tile load_rows has just been called for

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kGather ? 320 : 256, 1) fp8_few_any_kernel(con
             // this thread's row scale and the tiles' weight scales, as bits, a block ahead
             int srow = -1;  // -1: past the rows, or outside `a` (few_output drops those)
             if (tid < q.nv) {
-                srow = kGather ? __ldg(a.gather + q.m0 + tid) : q.m0 + tid;
+                srow = kGather ? load_now(a.gather + q.m0 + tid) : q.m0 + tid;
                 if (srow >= a.rows) srow = -1;
             }
             size_t wi[C::kAcc];

@@ -34,8 +34,8 @@ __device__ __forceinline__ void load_e8m0_x4(const uint8_t *p, size_t i, int las
     const uintptr_t q = reinterpret_cast<uintptr_t>(p + i);
     const uint32_t *w = reinterpret_cast<const uint32_t *>(q & ~(uintptr_t)3);
     const uint32_t skip = (uint32_t)q & 3u;
-    r0 = __ldg(w);
-    r1 = skip + (uint32_t)min(last, 3) > 3u ? __ldg(w + 1) : 0u;
+    r0 = load_now(w);
+    r1 = skip + (uint32_t)min(last, 3) > 3u ? load_now(w + 1) : 0u;
     shifts = shifts << 5 | skip << 3;
 }
 // field: 0 for the last one loaded, 1 for the one before, ...

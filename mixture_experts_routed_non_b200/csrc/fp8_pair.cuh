@@ -130,15 +130,6 @@ struct PTiles {
     }
 };
 
-// A load that stays behind the wait for the kernel before (the read-only loads may be moved
-// ahead of it by the compiler).
-template <typename T>
-__device__ __forceinline__ T load_now(const T *p) {
-    static_assert(sizeof(T) == 4, "a 32-bit word");
-    T v;
-    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
 // Segment offsets into off_s, held inside [0, P] whatever the caller's table says.
 __device__ __forceinline__ void load_offsets(const Fp8GemmArgs &a, int *off_s, int threads) {
     for (int i = threadIdx.x; i <= a.E; i += threads)
@@ -215,7 +206,7 @@ __device__ __forceinline__ void gather_rows(const Fp8GemmArgs &a, const PTiles<f
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int p = t.m0 + rank * 128 + r0 + 16 * i;
-            row[i] = p < t.m_end ? (int)min((long long)max(__ldg(a.gather + p), 0), (long long)a.rows - 1) : -1;
+            row[i] = p < t.m_end ? (int)min((long long)max(load_now(a.gather + p), 0), (long long)a.rows - 1) : -1;
         }
         for (int kb = 0; kb < a.nk; ++kb) {
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort))) {
@@ -300,7 +291,7 @@ __device__ __forceinline__ void pair_output(const Fp8GemmArgs &a, const PTile &t
     const int p = row0 + lane;
     const bool store = p < t.m_end;
     if (kGather && p < t.m_end) {  // a gathered row outside `a` counts as zeros
-        const int src = __ldg(a.gather + p);
+        const int src = load_now(a.gather + p);
         if (src < 0 || src >= a.rows) {
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0.f;
