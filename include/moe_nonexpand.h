@@ -611,6 +611,18 @@ MOE_API int moe_fp8_forward(const void *x, const void *x_scale, int32_t x_scale_
                             int32_t w2_scale_dtype, const void *b2, int32_t activation, int32_t gate_up_layout,
                             void *out, const moe_meta_t *meta_out, void *ws, size_t ws_bytes, moe_stream_t stream);
 
+/*
+ * Which kernel a product takes (for inspection and tests; nothing is launched): P
+ * rows in E segments (E = 0: one, moe_fp8_linear), the up product of
+ * moe_fp8_forward (swiglu, N = 2I) or any other, both scales e8m0 or not
+ * (f32_scales).  *chunk: rows of a segment to a unit of the few-row kernels, or 0
+ * for tiles of 256 x 256 on CTA pairs; *split: CTAs (pairs) that share a unit's
+ * K.  For a device of num_sms SMs on which clusters[i] clusters of 2, 4 and 8
+ * CTAs run at once, or (num_sms 0, clusters NULL) for the current device.
+ */
+MOE_API int moe_fp8_product_plan(int32_t swiglu, int32_t f32_scales, int64_t P, int32_t K, int32_t N, int32_t E,
+                                 int32_t num_sms, const int32_t *clusters, int32_t *chunk, int32_t *split);
+
 /* Byte offsets of the workspace's internal arrays (for inspection and tests).
  * Offsets of arrays that the given sizes do not need are 0. */
 typedef struct moe_ws_layout_t {

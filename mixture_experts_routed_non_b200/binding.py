@@ -75,6 +75,7 @@ EXPORTED = (
     "moe_fp8_grouped_linear",
     "moe_fp8_forward_workspace_bytes",
     "moe_fp8_forward",
+    "moe_fp8_product_plan",
     "moe_fp8_selftest_wait_timeout",
     "moe_add_rmsnorm_selftest_wait_timeout",
 )
@@ -224,6 +225,8 @@ def load() -> ctypes.CDLL:
     lib.moe_fp8_forward.restype = ctypes.c_int
     lib.moe_fp8_forward.argtypes = [P, P, i32, R, i32, i32, i32, P, P, i32, P, P, P, i32, P, i32, i32, P,
                                     ctypes.POINTER(MoeMeta), P, sz, P]
+    lib.moe_fp8_product_plan.restype = ctypes.c_int
+    lib.moe_fp8_product_plan.argtypes = [i32, i32, i64, i32, i32, i32, i32, P, P, P]
     lib.moe_fp8_selftest_wait_timeout.restype = ctypes.c_int
     lib.moe_fp8_selftest_wait_timeout.argtypes = [i32, i32, P, P, ctypes.c_uint32, P]
     lib.moe_add_rmsnorm_selftest_wait_timeout.restype = ctypes.c_int
@@ -1183,6 +1186,17 @@ def forward_fp8(x: torch.Tensor, x_scale: torch.Tensor, expert_idx: torch.Tensor
              w1.data_ptr(), w1_scale.data_ptr(), s1, _ptr(b1), w2.data_ptr(), w2_scale.data_ptr(), s2, _ptr(b2),
              ACT_SWIGLU, layout, out.data_ptr(), ctypes.byref(m) if m is not None else None, ws.data_ptr(), ws.numel())
     return out
+
+
+def product_plan_fp8(P: int, K: int, N: int, E: int = 0, *, swiglu: bool = False, f32: bool = False, num_sms: int = 0,
+                     clusters: Optional[Sequence[int]] = None):
+    """(chunk, split) of the kernel an 8-bit product takes (moe_fp8_product_plan), for tests: of
+    linear_fp8 (E = 0), grouped_linear_fp8, or forward_fp8's up product (swiglu, N = 2I)."""
+    c = (ctypes.c_int32 * 3)(*clusters) if clusters is not None else None
+    chunk, split = ctypes.c_int32(), ctypes.c_int32()
+    _check(load().moe_fp8_product_plan(int(swiglu), int(f32), P, K, N, E, num_sms, c, ctypes.byref(chunk),
+                                       ctypes.byref(split)), "moe_fp8_product_plan")
+    return chunk.value, split.value
 
 
 def selftest_fp8_wait_timeout(pairs: bool, lose: bool, timeout_us: int, device="cuda",

@@ -53,6 +53,13 @@ inline bool fp8_sizes_ok(int64_t P, int32_t E, int32_t K, int32_t N) {
     return units < INT32_MAX / 2 && (int64_t)K * N < ((int64_t)1 << 39);
 }
 cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);       // picks the kernel
+// The kernel picked: chunks of so many rows (0: pairs), and how many CTAs (pairs) share a unit's (tile's) K.  fit:
+// how many clusters of 2, 4 and 8 CTAs run at once, a byte each (fp8_clusters: on the current device).
+struct Fp8Plan {
+    int chunk, split;
+};
+Fp8Plan fp8_plan(int mode, const Fp8GemmArgs &a, int num_sms, int fit);
+cudaError_t fp8_clusters(int *fit);
 // few rows, e8m0; chunk: 32 or 64 rows, or 128 of one segment
 cudaError_t launch_fp8_few_gemm(int mode, Fp8GemmArgs &a, int chunk, int num_sms, cudaStream_t s);
 cudaError_t launch_fp8_pair_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s);     // 256-row tiles, any scales

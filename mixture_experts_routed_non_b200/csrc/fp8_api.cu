@@ -189,3 +189,36 @@ extern "C" MOE_API int moe_fp8_grouped_linear(const void *a, const void *a_scale
     return product(a, a_scale, a_scale_dtype, rows, K, gather, P, expert_off, E, w, w_scale, w_scale_dtype, N, bias,
                    out, err_word, stream);
 }
+
+extern "C" MOE_API int moe_fp8_product_plan(int32_t swiglu, int32_t f32_scales, int64_t P, int32_t K, int32_t N, int32_t E,
+                                            int32_t num_sms, const int32_t *clusters, int32_t *chunk, int32_t *split) {
+    if (!chunk || !split || P < 1 || P >= kMaxRows || E < 0 || E > kMaxExperts || num_sms < 0) return MOE_ERR_ARG;
+    if ((num_sms > 0) != (clusters != nullptr) || (swiglu && E == 0)) return MOE_ERR_ARG;
+    if (K < 16 || K % 16 != 0 || N < 8 || N % (swiglu ? 256 : 8) != 0 || K > (1 << 28) || N > (1 << 28)) return MOE_ERR_SHAPE;
+    if (!fp8_sizes_ok(P, E ? E : 1, K, N)) return MOE_ERR_SHAPE;
+    int sms = num_sms, fit = 0;
+    if (!clusters) {
+        const int st = current_device_sms(&sms);
+        if (st) return st;
+        if (fp8_clusters(&fit) != cudaSuccess) return MOE_ERR_CUDA;
+    } else {
+        for (int i = 0; i < 3; ++i) {
+            if (clusters[i] < 0 || clusters[i] > 255) return MOE_ERR_ARG;
+            fit |= clusters[i] << (8 * i);
+        }
+    }
+    const int32_t offsets = 0;  // (only whether there are segments matters)
+    Fp8GemmArgs g;
+    memset(&g, 0, sizeof g);
+    g.expert_off = E ? &offsets : nullptr;
+    g.a_f32 = g.w_f32 = f32_scales != 0;
+    g.P = P;
+    g.E = E ? E : 1;
+    g.K = K;
+    g.N = N;
+    g.nk = scale_blocks(K);
+    const Fp8Plan p = fp8_plan(swiglu ? kFp8SwiGlu : kFp8Bf16, g, sms, fit);
+    *chunk = p.chunk;
+    *split = p.split;
+    return MOE_OK;
+}

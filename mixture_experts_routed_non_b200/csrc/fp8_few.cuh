@@ -359,16 +359,21 @@ inline int few_split(int64_t units, int nk, int fit) {
     return S;
 }
 
+// Units of chunks of cn rows: of one segment; else the most there can be (no more than P / cn chunks and one
+// begun per expert).
+inline int64_t few_units(int mode, const Fp8GemmArgs &a, int cn) {
+    const int64_t chunks = a.expert_off ? a.P / cn + (a.E < a.P ? a.E : a.P) : (a.P + cn - 1) / cn;
+    return chunks * (mode == kFp8SwiGlu ? a.N / (2 * kFM) : (a.N + kFM - 1) / kFM);
+}
+
 // Launches a few-row kernel with chunks of cn rows on as many CTAs as there can be
 // units, split over K where there are few.
-inline cudaError_t launch_few(void (*kernel)(Fp8GemmArgs), Fp8GemmArgs &a, int cn, int n_tiles, int threads, size_t smem,
+inline cudaError_t launch_few(void (*kernel)(Fp8GemmArgs), int mode, Fp8GemmArgs &a, int cn, int threads, size_t smem,
                               int num_sms, cudaStream_t s) {
     int fit = 0;
     const cudaError_t err = few_setup(kernel, threads, smem, &fit);
     if (err != cudaSuccess) return err;
-    // one segment: its chunks; else no more than P / cn and one begun per expert
-    const int64_t chunks = a.expert_off ? a.P / cn + (a.E < a.P ? a.E : a.P) : (a.P + cn - 1) / cn;
-    const int64_t units = chunks * n_tiles;
+    const int64_t units = few_units(mode, a, cn);
     const int S = few_split(units, a.nk, fit);
     a.split = S;
     int64_t clusters = num_sms / S;

@@ -399,8 +399,7 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     using C = FCfg<CN, kMode>;
     auto *kernel = fp8_few_kernel<CN, kMode, kGather, kOne>;
     if (!make_few_maps(a, CN, !kGather)) return cudaErrorInvalidValue;
-    return launch_few(kernel, a, CN, kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM, kGather ? 448 : 384, C::kSmem,
-                      num_sms, s);
+    return launch_few(kernel, kMode, a, CN, kGather ? 448 : 384, C::kSmem, num_sms, s);
 }
 
 }  // namespace

@@ -323,8 +323,7 @@ cudaError_t launch_one(Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
     using C = QCfg<kMode>;
     auto *kernel = fp8_few_any_kernel<kMode, kGather, kOne>;
     if (!make_few_maps(a, CN, !kGather)) return cudaErrorInvalidValue;
-    return launch_few(kernel, a, CN, kMode == kFp8SwiGlu ? a.N / 256 : (a.N + kFM - 1) / kFM, kGather ? 320 : 256,
-                      C::kSmem, num_sms, s);
+    return launch_few(kernel, kMode, a, CN, kGather ? 320 : 256, C::kSmem, num_sms, s);
 }
 
 // Few rows, a scale in fp32.
@@ -381,44 +380,66 @@ constexpr Kernels kE8m0Times[] = {{32, 0, 4.6f, 0.275f}, {64, 0, 5.7f, 0.295f}, 
 constexpr Kernels kF32Times[] = {{32, 0, 4.0f, 0.385f}, {0, 1, 5.7f, 0.49f}, {0, 2, 9.5f, 0.49f}, {0, 4, 11.0f, 0.49f}};
 
 // Units (tiles) of one segment, or the most that segments can make.
-int64_t units_of(const Kernels &k, const Fp8GemmArgs &a) {
-    const int64_t rows = k.chunk ? k.chunk : kPM, cols = k.chunk ? kFM : kPN;
-    const int64_t pieces = a.expert_off ? a.P / rows + (a.E < a.P ? a.E : a.P) : (a.P + rows - 1) / rows;
-    return pieces * ((a.N + cols - 1) / cols);
+int64_t units_of(const Kernels &k, int mode, const Fp8GemmArgs &a) {
+    if (k.chunk) return few_units(mode, a, k.chunk);
+    return (a.expert_off ? a.P / kPM + (a.E < a.P ? a.E : a.P) : (a.P + kPM - 1) / kPM) * ((a.N + kPN - 1) / kPN);
 }
-float expected_us(const Kernels &k, const Fp8GemmArgs &a, int num_sms, int fit) {
-    const int64_t units = units_of(k, a);
+float expected_us(const Kernels &k, int mode, const Fp8GemmArgs &a, int num_sms, int fit) {
+    const int64_t units = units_of(k, mode, a);
     const int S = k.chunk ? few_split(units, a.nk, fit) : k.pairs, at_once = k.chunk ? num_sms / S : num_sms / 2;
     const float waves = (float)((units + at_once - 1) / at_once);
-    return k.start + k.block * waves * (float)((a.nk + S - 1) / S) + (S == 1 || !k.chunk ? 0.f : S < 8 ? 2.2f : 3.5f);
+    // A few-row unit with SwiGLU has two weight tiles: twice the bytes of a block, which is what bounds
+    // it with e8m0 scales; with fp32 scales the hand-over does, of both tiles at once.  (Layers of 1 to
+    // 32 experts with 4 to 128 rows each, e8m0: on average 0.6 % slower than with the best kernel, 1.3 %
+    // without the factor; fp32: 0.5 %, with the factor 1.3 %.)
+    const float block = k.chunk && mode == kFp8SwiGlu && !a.a_f32 && !a.w_f32 ? 2.f * k.block : k.block;
+    return k.start + block * waves * (float)((a.nk + S - 1) / S) + (S == 1 || !k.chunk ? 0.f : S < 8 ? 2.2f : 3.5f);
+}
+// Segments whose chunks of 32 fit one to an SM, and one segment: the kernel of least expected time.
+bool by_time(int mode, const Fp8GemmArgs &a, int num_sms) {
+    return !a.expert_off || units_of(kF32Times[0], mode, a) <= num_sms;
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
-    if (a.P == 0 || a.N == 0) return cudaSuccess;
+Fp8Plan fp8_plan(int mode, const Fp8GemmArgs &a, int num_sms, int fit) {
     const bool e8m0 = !a.a_f32 && !a.w_f32;
-    int chunk = 0;  // rows per chunk of the few-row kernels; 0: pairs
-    if (!a.expert_off || units_of(kF32Times[0], a) <= num_sms) {
-        int fit = 0;
-        const cudaError_t err = any_few_setup(&fit);
-        if (err != cudaSuccess) return err;
+    Fp8Plan p = {0, 1};
+    if (mode == kFp8SwiGlu && a.P <= 16ll * a.E) {
+        // (the lines are fitted on full chunks, whose SwiGLU and output take a microsecond longer: 8 experts of 4 rows,
+        // H 2048, I 768: layer 28.2 us, in tiles 29.9)
+        p.chunk = 32;
+    } else if (by_time(mode, a, num_sms)) {
         float least = 0.f;
         auto pick = [&](const Kernels &k) {
             if ((k.chunk == 128 || k.pairs > 1) && a.expert_off) return;
             // pairs share a tile where all their clusters run at once and each keeps a group of four blocks
-            if (k.pairs > 1 && (a.nk < 4 * k.pairs || units_of(k, a) > ((fit >> (4 * k.pairs)) & 255))) return;
-            const float us = expected_us(k, a, num_sms, fit);
-            if (least == 0.f || us < least) least = us, chunk = k.chunk, a.split = k.pairs;
+            if (k.pairs > 1 && (a.nk < 4 * k.pairs || units_of(k, mode, a) > ((fit >> (4 * k.pairs)) & 255))) return;
+            const float us = expected_us(k, mode, a, num_sms, fit);
+            if (least == 0.f || us < least) least = us, p.chunk = k.chunk, p.split = k.pairs;
         };
         if (e8m0) for (const Kernels &k : kE8m0Times) pick(k);
         else for (const Kernels &k : kF32Times) pick(k);
     } else {
-        if (!e8m0) chunk = a.P <= 32ll * a.E ? 32 : 0;
-        else chunk = a.P <= 16ll * a.E ? 32 : a.P <= 48ll * a.E ? 64 : 0;
+        if (!e8m0) p.chunk = a.P <= 32ll * a.E ? 32 : 0;
+        else p.chunk = a.P <= 16ll * a.E ? 32 : a.P <= 48ll * a.E ? 64 : 0;
     }
-    if (e8m0) return chunk ? launch_fp8_few_gemm(mode, a, chunk, num_sms, s) : launch_fp8_mx_pair_gemm(mode, a, num_sms, s);
-    return chunk ? launch_any_few(mode, a, num_sms, s) : launch_fp8_pair_gemm(mode, a, num_sms, s);
+    if (p.chunk) p.split = few_split(few_units(mode, a, p.chunk), a.nk, fit);
+    return p;
+}
+
+cudaError_t fp8_clusters(int *fit) { return any_few_setup(fit); }
+
+cudaError_t launch_fp8_gemm(int mode, Fp8GemmArgs &a, int num_sms, cudaStream_t s) {
+    if (a.P == 0 || a.N == 0) return cudaSuccess;
+    int fit = 0;
+    const cudaError_t err = any_few_setup(&fit);
+    if (err != cudaSuccess) return err;
+    const Fp8Plan p = fp8_plan(mode, a, num_sms, fit);
+    a.split = p.split;
+    if (!a.a_f32 && !a.w_f32)
+        return p.chunk ? launch_fp8_few_gemm(mode, a, p.chunk, num_sms, s) : launch_fp8_mx_pair_gemm(mode, a, num_sms, s);
+    return p.chunk ? launch_any_few(mode, a, num_sms, s) : launch_fp8_pair_gemm(mode, a, num_sms, s);
 }
 
 }  // namespace moe
