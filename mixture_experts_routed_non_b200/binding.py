@@ -887,6 +887,13 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _i32(name: str, sizes: int):
+    """``sizes``: the sizes that the C call takes as int32, or-ed together (ctypes would drop the
+    bits above)."""
+    if sizes >> 31:
+        raise MoeError(MOE_ERR_SHAPE, name)
+
+
 def _need_dim(t: torch.Tensor, name: str, dim: int):
     if t.dim() != dim:
         raise ValueError(f"{name}: expected {dim} dimensions, got shape {tuple(t.shape)}")
@@ -962,6 +969,7 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     if len(shape) != 2:
         _need_dim(x, "x", 2)
     N, H = shape
+    _i32("moe_add_rmsnorm", H)
     dev = x.device
     bf16 = torch.bfloat16
     if not (x.dtype is bf16 and x.is_contiguous()):
@@ -1003,6 +1011,7 @@ def _nothing(key):
 
 @functools.lru_cache(maxsize=256)
 def add_rmsnorm_backward_workspace_bytes(N: int, H: int) -> int:
+    _i32("moe_add_rmsnorm_backward_workspace_bytes", H)
     n = load().moe_add_rmsnorm_backward_workspace_bytes(N, H)
     if n == 0:
         raise MoeError(MOE_ERR_SHAPE, "moe_add_rmsnorm_backward_workspace_bytes")
@@ -1021,6 +1030,7 @@ def add_rmsnorm_backward(dy: torch.Tensor, res: torch.Tensor, weight: torch.Tens
     if len(shape) != 2:
         _need_dim(dy, "dy", 2)
     N, H = shape
+    _i32("moe_add_rmsnorm_backward", H)
     dev = dy.device
     bf16 = torch.bfloat16
     if not (dy.dtype is bf16 and dy.is_contiguous()):
@@ -1047,6 +1057,7 @@ def quantize_rows_fp8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: 
     """x [M,K] bf16 -> (q [M,K] e4m3, scale [M, ceil(K/128)] e8m0) (moe_fp8_quantize_rows)."""
     _need_dim(x, "x", 2)
     M, K = x.shape
+    _i32("moe_fp8_quantize_rows", K)
     dev = x.device
     _ok(x, "x", torch.bfloat16, (M, K), dev)
     q = _given(q, "q", x, (M, K), _E4M3, stream)
@@ -1063,6 +1074,7 @@ def quantize_weight_fp8(w: torch.Tensor, q: Optional[torch.Tensor] = None, scale
         raise ValueError(f"w: expected [E,K,N] or [K,N], got shape {tuple(w.shape)}")
     lead = tuple(w.shape[:-2])
     K, N = w.shape[-2:]
+    _i32("moe_fp8_quantize_weight", K | N | (lead[0] if lead else 1))
     dev = w.device
     _ok(w, "w", torch.bfloat16, w.shape, dev)
     q = _given(q, "q", w, lead + (N, K), _E4M3, stream)
@@ -1084,6 +1096,7 @@ def linear_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
         _need_dim(w, "w", 2)
     M, K = shape
     N = w_shape[0]
+    _i32("moe_fp8_linear", K | N)
     dev = a.device
     if not (a.dtype is _E4M3 and a.is_contiguous()):
         _ok(a, "a", _E4M3, shape, dev)
@@ -1116,6 +1129,7 @@ def grouped_linear_fp8(a: torch.Tensor, a_scale: torch.Tensor, expert_off: torch
     _need_dim(w, "w", 3)
     rows, K = a.shape
     E, N, _ = w.shape
+    _i32("moe_fp8_grouped_linear", K | N | E)
     dev = a.device
     _ok(a, "a", _E4M3, (rows, K), dev)
     _ok(w, "w", _E4M3, (E, N, K), dev)
@@ -1139,6 +1153,7 @@ def grouped_linear_fp8(a: torch.Tensor, a_scale: torch.Tensor, expert_off: torch
 
 
 def fp8_workspace_bytes(r: MoeRouting, H: int, I: int, E: int) -> int:
+    _i32("moe_fp8_forward_workspace_bytes", H | I | E)
     n = load().moe_fp8_forward_workspace_bytes(ctypes.byref(r), H, I, E)
     if n == 0:
         raise MoeError(MOE_ERR_ARG, "moe_fp8_forward_workspace_bytes")
@@ -1163,6 +1178,7 @@ def forward_fp8(x: torch.Tensor, x_scale: torch.Tensor, expert_idx: torch.Tensor
     N, H = x.shape
     E, I2, _ = w1.shape
     I = I2 // 2
+    _i32("moe_fp8_forward", H | I2 | E)
     dev = x.device
     _ok(x, "x", _E4M3, (N, H), dev)
     _ok(w1, "w1", _E4M3, (E, 2 * I, H), dev)
@@ -1192,6 +1208,7 @@ def product_plan_fp8(P: int, K: int, N: int, E: int = 0, *, swiglu: bool = False
                      clusters: Optional[Sequence[int]] = None):
     """(chunk, split) of the kernel an 8-bit product takes (moe_fp8_product_plan), for tests: of
     linear_fp8 (E = 0), grouped_linear_fp8, or forward_fp8's up product (swiglu, N = 2I)."""
+    _i32("moe_fp8_product_plan", K | N | (E if E > 0 else 0))
     c = (ctypes.c_int32 * 3)(*clusters) if clusters is not None else None
     chunk, split = ctypes.c_int32(), ctypes.c_int32()
     _check(load().moe_fp8_product_plan(int(swiglu), int(f32), P, K, N, E, num_sms, c, ctypes.byref(chunk),

@@ -210,3 +210,40 @@ def test_scale_and_rounding_of_the_reference():
     assert torch.equal(ref.round_e4m3(v), v.float().to(E4).float().double())
     amax = torch.tensor([0.0, 448.0, 448.0001, 224.0, 1.75, 1.7501, 2.0 ** -140], dtype=torch.float64)
     assert ref.pow2_scale(amax).tolist() == [1.0, 1.0, 2.0, 0.5, 2.0 ** -8, 2.0 ** -7, 2.0 ** -126]
+
+
+def _big(shape, dtype):
+    """A tensor that has a shape but no memory."""
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """A size that the C entry point takes as int32 is refused, not cut to its low bits (2^32 + 256 -> 256)."""
+    b = (1 << 32) + 256
+    e, f32 = b // 128, torch.float32
+    idx, tw = torch.zeros((4, 2), dtype=torch.int32), torch.ones((4, 2))
+    r = binding.routing(idx, tw)
+    calls = [
+        lambda: binding.add_rmsnorm(_big((1, b), BF), _big((b,), BF)),
+        lambda: binding.add_rmsnorm_backward(_big((1, b), BF), _big((1, b), BF), _big((b,), BF), _big((1,), f32)),
+        lambda: binding.add_rmsnorm_backward_workspace_bytes(4, b),
+        lambda: binding.quantize_rows_fp8(_big((1, b), BF)),
+        lambda: binding.quantize_weight_fp8(_big((b, 16), BF)),
+        lambda: binding.quantize_weight_fp8(_big((2, 16, b), BF)),
+        lambda: binding.quantize_weight_fp8(_big((b, 16, 8), BF)),
+        lambda: binding.linear_fp8(_big((1, b), E4), _big((1, e), E8), _big((8, b), E4), _big((1, e), E8)),
+        lambda: binding.linear_fp8(_big((1, 16), E4), _big((1, 1), E8), _big((b, 16), E4), _big((e, 1), E8)),
+        lambda: binding.grouped_linear_fp8(_big((1, b), E4), _big((1, e), E8), _big((2,), torch.int32), _big((1, 8, b), E4),
+                                           _big((1, 1, e), E8)),
+        lambda: binding.grouped_linear_fp8(_big((1, 16), E4), _big((1, 1), E8), _big((b + 1,), torch.int32),
+                                           _big((b, 8, 16), E4), _big((b, 1, 1), E8)),
+        lambda: binding.forward_fp8(_big((4, b), E4), _big((4, e), E8), idx, tw, _big((2, 256, b), E4), _big((2, 2, e), E8),
+                                    _big((2, b, 128), E4), _big((2, e, 1), E8)),
+        lambda: binding.fp8_workspace_bytes(r, 256, b, 4),
+        lambda: binding.product_plan_fp8(4, b, 256, num_sms=148, clusters=(74, 33, 15)),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(binding.MoeError) as err:
+            call()
+            pytest.fail(f"call {i} was accepted")
+        assert err.value.status == SHAPE, i
