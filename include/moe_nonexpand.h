@@ -524,7 +524,7 @@ MOE_API int moe_ep_combine(const moe_ep_sources_t *src, const int32_t *send_idx,
  * exactly when residual is); y [N,H] bf16 or NULL; y8 [N,H] e4m3 and y8_scale
  * [N, ceil(H/128)] e8m0, or both NULL (at least one of y and y8); inv_rms [N]
  * fp32 or NULL (the backward reads it).  res may be residual or x itself, and
- * y may be x; no other buffers may overlap.  Sums are fp32; y is rounded once
+ * y may be x, but not both x; no other buffers may overlap.  Sums are fp32; y is rounded once
  * to each output type.  H a multiple of 8, at most 16384; eps >= 0; bf16 and
  * e4m3 buffers 16-byte aligned.  Should a wait inside the kernel give up, the
  * block's rows from there on are NaN in every output, res among them.  One kernel

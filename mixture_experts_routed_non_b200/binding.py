@@ -964,7 +964,7 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     for: "res" (s, with a residual), "y" (bf16), "y8" and "y8_scale" (``fp8``:
     e4m3 and e8m0 per 128 columns), "inv_rms" [N] (for add_rmsnorm_backward).
     ``out`` may hold buffers for any of them; out["res"] may be the residual
-    itself."""
+    or x itself, out["y"] may be x (not both x)."""
     shape = x.shape
     if len(shape) != 2:
         _need_dim(x, "x", 2)
@@ -1000,6 +1000,8 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
         for k in out:
             if k not in r:
                 raise ValueError(f"out: {k!r} is not written by this call")
+        if N and p_y is not None and p_y == p_res:
+            raise ValueError("out: y and res are the same buffer")
     _call_on(dev, stream, "moe_add_rmsnorm", x.data_ptr(), p_residual, weight.data_ptr(), N, H, eps, p_res, p_y, p_y8,
              p_scale, p_inv)
     return r

@@ -247,3 +247,10 @@ def test_binding_refuses_sizes_past_32_bits():
             call()
             pytest.fail(f"call {i} was accepted")
         assert err.value.status == SHAPE, i
+
+
+def test_norm_refuses_y_and_res_in_one_buffer():
+    """res may be x, and y may be x, but the second to be written would replace the first."""
+    x, w, r = torch.zeros((4, 256), dtype=BF), torch.ones(256, dtype=BF), torch.zeros((4, 256), dtype=BF)
+    with pytest.raises(ValueError, match="same buffer"):
+        binding.add_rmsnorm(x, w, r, out=dict(res=x, y=x))
