@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kNMaxT) add_rmsnorm_bwd_kernel(const NormBwdAr
             phase ^= 1u;
         }
         if (*(volatile uint32_t *)&gave_up) dot = __uint_as_float(0x7FC00000u);  // a load never came: NaN, not a wrong value
-        const float k = inv * inv * (dot * per_h);
+        const float k = inv * (inv * (dot * per_h));  // (inv^2 alone may pass the range)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = threadIdx.x + i * T;

@@ -56,3 +56,22 @@ def test_backward(N, H, with_dres):
     # at most 10, then 5 levels of a tree
     steps = 1 + (N // 296 + 1) + 15 + 10 + 5
     ref.check(got["dweight"], dw, steps * 2.0 ** -24 * 1.01 * (d * s * inv[:, None]).abs().sum(0) + 2.0 ** -140, "dweight")
+
+
+def test_backward_of_rows_whose_1_over_rms_squared_passes_the_range():
+    """1 / rms = 2^65: its square is no fp32 number, the gradient is."""
+    N, H = 5, 640
+    g = _gen(3)
+    sign = torch.where(torch.rand((N, H), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    x = (sign * 2.0 ** -65).to(torch.bfloat16)
+    x[3] = 1.0  # a row as usual beside them
+    w = (1 + 0.3 * torch.randn((H,), generator=g, device="cuda")).to(torch.bfloat16)
+    dy = torch.randn((N, H), generator=g, device="cuda").to(torch.bfloat16)
+    inv = binding.add_rmsnorm(x, w, eps=0.0, inv_rms=True)["inv_rms"]
+    assert bool((inv[:3] == 2.0 ** 65).all())
+    got = binding.add_rmsnorm_backward(dy, x, w, inv)
+    s, d, wd, i = x.double(), dy.double(), w.double(), inv.double()
+    dx, dw = ref.norm_backward(d, s, wd, i)
+    mag = (i[:, None] * wd * d).abs() + i[:, None] ** 3 * (d * wd * s).abs().mean(-1, keepdim=True) * s.abs()
+    ref.check(got["dx"], dx, 2.0 ** -8 * dx.abs() + 2 * FP32 * mag, "dx")
+    ref.check(got["dweight"], dw, 2.0 ** -18 * (d * s * i[:, None]).abs().sum(0), "dweight")
