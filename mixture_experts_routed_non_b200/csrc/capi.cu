@@ -1189,7 +1189,9 @@ extern "C" MOE_API const char *moe_nonexpand_strerror(int status) {
     switch (status) {
         case MOE_OK: return "ok";
         case MOE_ERR_ARG: return "invalid argument";
-        case MOE_ERR_SHAPE: return "unsupported shape (a size is out of range or no multiple of what the call needs)";
+        case MOE_ERR_SHAPE:
+            return "unsupported shape (a size is out of range or no multiple of what the call needs; the bf16 layer: H and "
+                   "I must be multiples of 64)";
         case MOE_ERR_WS: return "workspace missing, misaligned or too small";
         case MOE_ERR_CUDA: return "CUDA runtime or launch failure";
         case MOE_ERR_DEVICE: return "current device is not an sm_100 (B200-class) GPU";

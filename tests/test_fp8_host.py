@@ -254,3 +254,7 @@ def test_norm_refuses_y_and_res_in_one_buffer():
     x, w, r = torch.zeros((4, 256), dtype=BF), torch.ones(256, dtype=BF), torch.zeros((4, 256), dtype=BF)
     with pytest.raises(ValueError, match="same buffer"):
         binding.add_rmsnorm(x, w, r, out=dict(res=x, y=x))
+
+
+def test_message_of_a_bad_shape_names_the_bf16_multiple():
+    assert "multiples of 64" in binding.strerror(SHAPE)
