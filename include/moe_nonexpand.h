@@ -524,7 +524,8 @@ MOE_API int moe_ep_combine(const moe_ep_sources_t *src, const int32_t *send_idx,
  * exactly when residual is); y [N,H] bf16 or NULL; y8 [N,H] e4m3 and y8_scale
  * [N, ceil(H/128)] e8m0, or both NULL (at least one of y and y8); inv_rms [N]
  * fp32 or NULL (the backward reads it).  res may be residual or x itself, and
- * y may be x, but not both x; no other buffers may overlap.  Sums are fp32; y is rounded once
+ * y may be x, but not both x; no other buffers may overlap.  Sums are fp32 (a row
+ * whose squares add up past its range has inv_rms 0 and y 0); y is rounded once
  * to each output type.  H a multiple of 8, at most 16384; eps >= 0; bf16 and
  * e4m3 buffers 16-byte aligned.  Should a wait inside the kernel give up, the
  * block's rows from there on are NaN in every output, res among them.  One kernel
@@ -566,9 +567,11 @@ MOE_API int moe_fp8_quantize_weight(const void *w, int32_t E, int32_t K, int32_t
  * Product of 8-bit rows and an 8-bit weight, both scaled per block of 128:
  *   out[m,n] = bf16( sum_k a[m,k] w[n,k] + bias[n] )
  * a [M,K], w [N,K] e4m3 with their scales; bias [N] bf16 or NULL; out [M,N]
- * bf16.  Each block of 128 along K is summed by the tensor cores and added in
- * fp32 with its two scales; no long sum is held in less.  K a multiple of 16,
- * N of 8; a, w, out 16-byte aligned.  err_word: device uint32 (MOE_DEVERR_*
+ * bf16.  Sums are fp32.  With e8m0 scales on both sides the tensor cores apply
+ * them to the products and add up all of K (or a part of it, the parts then in a
+ * fixed order).  Where a scale is fp32 they sum each block of 128 bare, and its
+ * sum times the product of its two scales (rounded to fp32, whose range it has to
+ * keep) is added in fp32 registers.  K a multiple of 16, N of 8; a, w, out 16-byte aligned.  err_word: device uint32 (MOE_DEVERR_*
  * bits are OR-ed in, never cleared) or NULL.  Should a wait inside the kernel give
  * up (MOE_DEVERR_TIMEOUT), the output of the SMs concerned is NaN.  One kernel launch.
  */
@@ -596,7 +599,9 @@ MOE_API int moe_fp8_grouped_linear(const void *a, const void *a_scale, int32_t a
 /*
  * moe_nonexpand_routed_forward in 8 bits (inference): metadata, product up on
  * the rows of x with bias and SwiGLU, h requantised to e4m3 (e8m0 scale per
- * 128 columns, from the fp32 values), product down with bias, combine.
+ * 128 columns, from the fp32 values), product down with bias, combine.  Between
+ * the last two each row is held in fp16 scaled by a power of two per 32 columns,
+ * as in the bf16 forward.
  *   x [N,H] e4m3 + scales, w1 [E,2I,H], w2 [E,H,I] e4m3 + scales
  *   (moe_fp8_quantize_weight of the bf16 weights), b1 [E,2I], b2 [E,H] bf16 or
  *   NULL (b1 in w1's column order), out [N,H] bf16.

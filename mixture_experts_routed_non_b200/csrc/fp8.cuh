@@ -19,7 +19,11 @@ inline int scale_blocks(int64_t n) { return (int)((n + kScaleBlock - 1) / kScale
 enum Fp8Mode : int32_t {
     kFp8Bf16 = 0,    // out [P,N] bf16
     kFp8SwiGlu = 1,  // h = silu(gate) up as e4m3 [P,N/2] with an e8m0 scale per 128 columns
-    kFp8Y16 = 2,     // y [P,N] as fp16 scaled by a power of two per 32 columns (the combine's rows)
+    // y [P,N] as fp16 scaled by a power of two per 32 columns (the combine's rows, as the bf16 forward's): half
+    // the bytes of fp32, which the combine is bound by (95 us for 131072 x 2048), at 2^-11 of a value.  The
+    // layer's error against 64 bits goes from 1.664e-3 of its norm, nearly all of it the bf16 output's
+    // rounding, to 1.677e-3 (2048 tokens, H 2048, I 768, 128 experts, top 8).
+    kFp8Y16 = 2,
 };
 
 struct Fp8GemmArgs {

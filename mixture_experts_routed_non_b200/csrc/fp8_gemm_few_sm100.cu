@@ -5,10 +5,10 @@
 // fp8_gemm_mx_sm100.cu) and sums the unit's K in one TMEM accumulator; two
 // accumulators alternate between units.  Units, K split and epilogue: fp8_few.cuh.
 //
-// The ring (up to eight stages of 128 K) keeps 112 to 131 KB of weights in flight per
-// SM, 96 KB for SwiGLU in chunks of 64.  1 x 7168 x 4096: 9.6 us, 3.1 TB/s (ramp
+// The ring (up to eight stages of 128 K) keeps 131 KB of weights in flight per SM in chunks of
+// 32 rows, 98 KB in chunks of 64 and 66 KB of 128.  1 x 7168 x 4096: 9.0 us, 3.3 TB/s (ramp
 // and join of the split); 1024 skewed rows over 256 experts, K 512, N 2048: 32 us,
-// 77 % of what reading the experts in use costs.
+// 77 % of the rate at which the experts in use can be read.
 //
 // Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer, 2 = TMA of
 // the rows or gather relay, 3 idle, 4-7 = scales (one per TMEM lane quarter), 8-11 =

@@ -17,13 +17,13 @@
 // arrive as long as a block's MMAs).
 //
 // TMEM: the accumulator (256 columns) and four 16-column scale slots.  A second
-// accumulator does not fit beside them, so the epilogue first takes the whole
+// accumulator of this width does not fit beside them, so the epilogue first takes the whole
 // accumulator into registers (64 per thread) and hands it back; conversion and
 // stores run behind the next tile's MMAs.
 //
-// Bound by the tensor cores, and in long runs by their power: 8192 x 7168 x 4096 141
-// us (3.4 PFLOP/s), back to back 193; 131072 gathered rows over 128 experts, K 2048,
-// N 1536 367 us (2.2), back to back 469.
+// Bound by the tensor cores, and in long runs by their power: 8192 x 7168 x 4096 159
+// us in bursts of four (3.0 PFLOP/s), back to back 188; 131072 gathered rows over 128
+// experts, K 2048, N 1536 380 us (2.2), back to back 466.
 //
 // Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer (even
 // CTA), 2 = TMA of the rows or gather relay (fp8_gemm_pair_sm100.cu), 4-7 = scales, 8-23 = epilogue, 24-27 =

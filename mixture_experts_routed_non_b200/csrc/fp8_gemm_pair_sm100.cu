@@ -7,9 +7,9 @@
 // fill the other accumulator.  At the tensor cores' full rate a block takes 512
 // clocks; what bounds it here is the hand-over of an accumulator, about 1200
 // clocks of latency (barrier, TMEM load, arithmetic, barrier, in turn) that four
-// warps per scheduler hide in part (8192 x 7168 x 4096: 226 us = 2.1 PFLOP/s; with
-// eight warps of 128 columns 340, with power-of-two scales, which need none of
-// this, 141).
+// warps per scheduler hide in part (8192 x 7168 x 4096 in bursts of four: 233 us =
+// 2.1 PFLOP/s; with eight warps of 128 columns 340, with power-of-two scales, which
+// need none of this, 159).
 //
 // Warp roles: 0 = TMA of the weights, 1 = TMEM allocator and MMA issuer (even CTA),
 // 2 = TMA of the rows or gather relay, 3 = scale loader, 4-19 = epilogue, 20-23 =

@@ -15,7 +15,7 @@ __host__ __device__ constexpr uint32_t idesc_mx_e4m3(int M, int N) {
     return ((static_cast<uint32_t>(N) >> 3) << 17) | (1u << 23) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 __host__ __device__ constexpr uint32_t idesc_byte(int k) { return (uint32_t)k << 4 | (uint32_t)k << 29; }
-// 32 lanes x 4 (8) 32-bit TMEM columns from registers.
+// 32 lanes x 4 32-bit TMEM columns from registers.
 __device__ __forceinline__ void tmem_st_x4(uint32_t taddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r0), "r"(r1),
                  "r"(r2), "r"(r3)

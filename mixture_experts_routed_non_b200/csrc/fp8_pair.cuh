@@ -190,8 +190,8 @@ __device__ __forceinline__ void store32(const CUtensorMap *map, uint32_t buf, in
 // unconditionally -- a row outside `a` some other row (pair_output drops what it
 // gave), a piece past the end of K the row's last one (the weights are zeros
 // there) -- because a choice between two sources, or the copy's own zero fill,
-// cost a third to two thirds of the whole product (131072 x 2048 x 1536 over 128
-// experts: 358 us like this, 465 with a zero row, 547 with zero fill).
+// cost a quarter to a half of the whole product (131072 x 2048 x 1536 over 128
+// experts, when it was tried: 358 us like this, 465 with a zero row, 547 with zero fill).
 template <int kStages, typename Empty, typename Gfull>
 __device__ __forceinline__ void gather_rows(const Fp8GemmArgs &a, const PTiles<false> &list, int rank, int g, uint32_t base,
                                             Empty empty_bar, Gfull gfull_bar, volatile uint32_t *abort, int t0,

@@ -19,12 +19,14 @@
 //
 // Bound by HBM: one pass, every tensor read or written once.  Every kernel is a
 // programmatic dependent of the launch before it: its blocks come up and set their
-// barriers while that one ends.  Measured back to back (rates of the bytes that have
-// to move): 16384 x 2048 with residual, 8-bit out 43 us (5.5 TB/s; 45 without the early
-// start); 8191 x 7168 with residual, bf16 out 76 us (6.2 TB/s; 79); gradient of 16384
-// x 2048 with dres 48 us (5.6 TB/s; 49), its second kernel included.  Without a
-// residual the 8-bit form has half as many bytes to an instruction and is bound by issuing
-// them: 16384 x 2048 29 us (3.5 TB/s; 32 with two products per value and IEEE divisions).
+// barriers while that one ends.  Measured back to back in a graph (rates of the bytes that have
+// to move): 16384 x 2048 with residual, 8-bit out 42 us (5.7 TB/s; 45 without the early
+// start); 8191 x 7168 with residual, bf16 out 77 us (6.1 TB/s; 79); gradient of 16384
+// x 2048 with dres 47 us (5.7 TB/s; 49), its second kernel included.  Without a
+// residual the 8-bit form has half as many bytes to an instruction and issues most of the
+// time: 16384 x 2048 29 us (3.5 TB/s; 32 with two products per value and IEEE divisions), 65536 x 2048
+// 109 us with 21 instructions a value, polling included, the schedulers busy 74 % of the cycles and
+// DRAM 42 %.
 #include "fp8.cuh"
 
 namespace moe {
