@@ -691,7 +691,7 @@ MOE_API int moe_fp8_selftest_wait_timeout(int32_t pairs, int32_t lose, void *out
                                           uint32_t timeout_us, moe_stream_t stream);
 
 /*
- * And for the norm with a residual (H at most 256): one block takes all N rows,
+ * And for the norm with a residual (H at most 256, N 1 to 4096): one block takes all rows,
  * and from its third turn on (32 rows of up to 128 columns, 16 of more) the loads
  * never come.  Those rows are NaN in res, y and inv_rms.
  */

@@ -99,7 +99,7 @@ extern "C" MOE_API int moe_add_rmsnorm(const void *x, const void *residual, cons
 extern "C" MOE_API int moe_add_rmsnorm_selftest_wait_timeout(const void *x, const void *residual, const void *weight,
                                                              int64_t N, int32_t H, float eps, void *res, void *y,
                                                              float *inv_rms, moe_stream_t stream) {
-    if (N < 1 || !residual || !y) return MOE_ERR_ARG;
+    if (N < 1 || N > 4096 || !residual || !y) return MOE_ERR_ARG;  // (every turn behind the lost one polls a while)
     if (H > 256) return MOE_ERR_SHAPE;
     NormArgs a;
     int sms = 0;
