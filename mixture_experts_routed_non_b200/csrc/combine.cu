@@ -34,11 +34,20 @@ constexpr int kCombineThreads = 256;
 constexpr int kTokPerBlock = 32;
 constexpr int kStagedPairs = 256;  // pair indices staged in shared memory per block (28 tokens of 8 pairs fit)
 
+// Rows of y.  The launch that this one overlaps (pdl_wait) writes them and their exponents: no read-only
+// loads, which take memory that nobody writes while the kernel runs.
 __device__ __forceinline__ uint4 ld_stream_v4(const void *p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
+    return v;
+}
+
+// The exponent of a block of a row.
+__device__ __forceinline__ int ld_exponent(const int8_t *p) {
+    int v;
+    asm volatile("ld.global.s8 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
 
@@ -101,7 +110,7 @@ __device__ __forceinline__ void combine_tokens(const uint16_t *__restrict__ y, c
                 const int q = base + u;
                 const int row = q < np ? (kStaged ? pidx[q] : __ldg(pidx + q)) : 0;
                 v[u] = q < np ? ld_stream_v4(ycol + (size_t)row * H) : make_uint4(0, 0, 0, 0);
-                if (kScaled) ex[u] = q < np ? (int)__ldg(scol + (size_t)row * sld) : 0;
+                if (kScaled) ex[u] = q < np ? ld_exponent(scol + (size_t)row * sld) : 0;
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {

@@ -17,3 +17,10 @@ def test_no_read_only_load_of_what_the_launch_before_may_write(name):
         code = re.sub(r"//[^\n]*", "", f.read())
     found = re.findall(r"[^\n]*(?:__ldg\s*\(|ld\.global\.nc)[^\n]*", code)
     assert not found, found
+
+
+def test_the_combine_reads_y_by_plain_loads():
+    """It overlaps the product that writes y and its exponents (the metadata's tables are finished by then)."""
+    with open(os.path.join(CSRC, "combine.cu")) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert "ld.global.nc" not in code and not re.search(r"__ldg\s*\(\s*(y|scol|y_scale)", code)
