@@ -571,9 +571,11 @@ MOE_API int moe_fp8_quantize_weight(const void *w, int32_t E, int32_t K, int32_t
  * them to the products and add up all of K (or a part of it, the parts then in a
  * fixed order).  Where a scale is fp32 they sum each block of 128 bare, and its
  * sum times the product of its two scales (rounded to fp32, whose range it has to
- * keep) is added in fp32 registers.  K a multiple of 16, N of 8; a, w, out 16-byte aligned.  err_word: device uint32 (MOE_DEVERR_*
- * bits are OR-ed in, never cleared) or NULL.  Should a wait inside the kernel give
- * up (MOE_DEVERR_TIMEOUT), the output of the SMs concerned is NaN.  One kernel launch.
+ * keep) is added in fp32 registers.  K a multiple of 16, N of 8; a, w, out
+ * 16-byte aligned.  err_word: device uint32 (MOE_DEVERR_* bits are OR-ed in,
+ * never cleared) or NULL.  Should a wait inside the kernel give up
+ * (MOE_DEVERR_TIMEOUT), the output of the SMs concerned is NaN.  One kernel
+ * launch.
  */
 MOE_API int moe_fp8_linear(const void *a, const void *a_scale, int32_t a_scale_dtype, int64_t M, int32_t K,
                            const void *w, const void *w_scale, int32_t w_scale_dtype, int32_t N, const void *bias,

@@ -12,8 +12,9 @@ def test_selftest_refuses(bad):
     assert binding.load().moe_fp8_selftest_wait_timeout(*{**kw, **bad}.values()) == binding.MOE_ERR_ARG
 
 
-@pytest.mark.parametrize("bad,status", [(dict(x=None), "ARG"), (dict(residual=None), "ARG"), (dict(res=None), "ARG"),
-                                        (dict(y=None), "ARG"), (dict(N=0), "ARG"), (dict(N=4097), "ARG"), (dict(H=264), "SHAPE"), (dict(H=12), "SHAPE")])
+@pytest.mark.parametrize("bad,status", [
+    (dict(x=None), "ARG"), (dict(residual=None), "ARG"), (dict(res=None), "ARG"), (dict(y=None), "ARG"), (dict(N=0), "ARG"),
+    (dict(N=4097), "ARG"), (dict(H=264), "SHAPE"), (dict(H=12), "SHAPE")])
 def test_norm_selftest_refuses(bad, status):
     kw = dict(x=A, residual=A, weight=A, N=4, H=128, eps=1e-6, res=A, y=A, inv_rms=A, stream=None)
     st = binding.load().moe_add_rmsnorm_selftest_wait_timeout(*{**kw, **bad}.values())
